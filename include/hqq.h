@@ -399,6 +399,59 @@ int hqq_lowrank_noalloc(const void* W, const void* packed, const void* scale, co
 /* Bytes of the fixed scratch array of hqq_lowrank_noalloc. */
 int64_t hqq_lowrank_noalloc_max_bytes(void);
 
+/* Element types of the entry points that take more than fp16. */
+typedef enum hqq_dtype {
+    HQQ_F16 = 0,
+    HQQ_BF16 = 1,
+    HQQ_F32 = 2
+} hqq_dtype;
+
+/*
+ * hqq_distill -- distillation loss against a teacher's stored top logits, and
+ * its gradient with respect to the student's logits.
+ *
+ * Per token i, with z = logits[i] / temperature over the vocabulary and the
+ * teacher's valid entries k (0 <= top_index[i, k] < vocab; others are unused):
+ *   log p_k = top_logits[i, k] / temperature - L_i, where L_i is teacher_lse[i]
+ *             or, when that is NULL, the log-sum-exp of the valid entries
+ *             (the p_k then sum to 1);
+ *   loss[i] = weight[i] * sum_k p_k * (log p_k - log softmax(z)[top_index[i, k]]);
+ *   grad[i, v] = d loss[i] / d logits[i, v]
+ *           = weight[i] / temperature * (sum_k p_k * softmax(z)[v]
+ *                                        - sum of the p_k with top_index v).
+ * Computed in fp32 from one read of the logits; grad is rounded once to the
+ * logits' type.  Results do not depend on execution order.
+ *  - An index may occur several times: its p_k add up in the gradient, and the
+ *    loss takes each entry as given.  An entry whose value is -inf has p_k = 0.
+ *  - A token without a valid entry has loss 0 and gradient 0.
+ *  - A token of weight 0 (padding, prompt) is not read: loss 0, lse 0, gradient
+ *    0, whatever its logits hold.
+ *  - A logit of -inf has probability 0; a token whose logits are all -inf, or
+ *    hold a NaN or +inf, gets NaN, and no other token does.
+ *   logits     [in]  `dtype` [tokens, vocab], rows logits_stride elements apart
+ *                    (>= vocab), aligned to its element.
+ *   top_logits [in]  `top_dtype` [tokens, top_k], dense.
+ *   top_index  [in]  int32 or int64 (index_bytes 4 or 8) [tokens, top_k], dense.
+ *   teacher_lse [in] fp32 [tokens] or NULL: the teacher's log-sum-exp over its
+ *                    whole vocabulary at the same temperature.
+ *   weight     [in]  fp32 [tokens] or NULL (all 1).
+ *   loss, lse  [out] fp32 [tokens] or NULL; lse[i] = log-sum-exp of z.
+ *   grad       [out] `dtype` [tokens, vocab], rows grad_stride elements apart,
+ *                    or NULL.  May be the logits themselves (same pointer and
+ *                    stride); must not overlap them in another way.
+ * vocab and top_k are at least 1, vocab below 2^31, top_k at most 1024, tokens
+ * below 2^27.  The kernel is fastest where logits, grad and their rows are
+ * 16-byte aligned.
+ * Errors: HQQ_ERR_SHAPE, HQQ_ERR_UNSUPPORTED (dtype, index_bytes),
+ * HQQ_ERR_PARAM (temperature not > 0 and finite), HQQ_ERR_NULL, HQQ_ERR_ALIGN,
+ * HQQ_ERR_CUDA.
+ */
+int hqq_distill(const void* logits, int64_t logits_stride, int dtype, int64_t tokens,
+                int64_t vocab, const void* top_logits, int top_dtype, const void* top_index,
+                int index_bytes, int64_t top_k, float temperature, const float* teacher_lse,
+                const float* weight, float* loss, float* lse, void* grad, int64_t grad_stride,
+                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,7 @@ __all__ = ["HQQError", "hqq_quantize", "hqq_quantize_ex", "hqq_quantize_half", "
            "hqq_packed_bytes", "hqq_status_string", "QuantizedMatrix", "LIB_PATH",
            "Meta8", "hqq_meta_groups", "hqq_meta_quantize", "hqq_meta_quantize_batch",
            "hqq_meta_dequantize",
-           "hqq_dequantize_meta", "hqq_linear", "hqq_linear_meta",
+           "hqq_dequantize_meta", "hqq_linear", "hqq_linear_meta", "hqq_lowrank", "hqq_distill",
            "DEFAULT_P", "DEFAULT_BETA", "DEFAULT_KAPPA", "DEFAULT_ITERS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +78,9 @@ _lib.hqq_lowrank_workspace_bytes.restype = _I64
 _lib.hqq_lowrank.argtypes = [_P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                              _I64, _P]
 _lib.hqq_lowrank.restype = _I
+_lib.hqq_distill.argtypes = [_P, _I64, _I, _I64, _I64, _P, _I, _P, _I, _I64, _F, _P, _P, _P, _P,
+                             _P, _I64, _P]
+_lib.hqq_distill.restype = _I
 
 
 class HQQError(RuntimeError):
@@ -402,3 +405,80 @@ def hqq_lowrank(W, q: QuantizedMatrix, rank: int, omega, power_iters: int = 2, w
                             _ptr(A), _ptr(sigma), _ptr(workspace), workspace.numel(),
                             _stream(stream)))
     return B, A, sigma
+
+
+def _dtype_code(dtype, name):
+    """hqq_dtype of a torch dtype."""
+    import torch
+    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32")
+    return code
+
+
+def _on_device_of(t, stream, *others):
+    """Check that the given tensors live on t's device, and return (context
+    that makes it the current device, stream handle there)."""
+    import torch
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"all tensors must be on {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream must be on {t.device}")
+    return torch.cuda.device(t.device), ctypes.c_void_p(stream.cuda_stream)
+
+
+def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher_lse=None,
+                weight=None, grad=False, loss=None, lse=None, stream=None):
+    """Distillation loss of student ``logits`` [tokens, vocab] (fp16, bf16 or
+    fp32; rows may be strided) against a teacher's stored entries
+    ``top_logits`` / ``top_index`` [tokens, top_k] (index int32 or int64; an index
+    outside the vocabulary is unused), and its gradient (see include/hqq.h).
+    ``teacher_lse`` is the teacher's log-sum-exp over its whole vocabulary
+    (without it the entries are normalised to sum 1), ``weight`` a factor per
+    token (0: the token is skipped).  ``grad`` is False, True, or the tensor to
+    write the gradient to, which may be ``logits`` itself.  Returns
+    (loss [tokens], lse [tokens], gradient or None)."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA [tokens, vocab] tensor with adjacent columns")
+    dt = _dtype_code(logits.dtype, "logits")
+    tokens, vocab = logits.shape
+    if top_logits.dim() != 2 or top_logits.shape != top_index.shape or \
+            top_logits.shape[0] != tokens:
+        raise ValueError("top_logits and top_index must be [tokens, top_k] tensors")
+    if top_index.dtype not in (torch.int32, torch.int64):
+        raise ValueError("top_index must be int32 or int64")
+    for t, nm in ((top_logits, "top_logits"), (top_index, "top_index"),
+                  (teacher_lse, "teacher_lse"), (weight, "weight"), (loss, "loss"), (lse, "lse")):
+        _check_tensor(t, nm)
+    for t, nm in ((teacher_lse, "teacher_lse"), (weight, "weight"), (loss, "loss"), (lse, "lse")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != tokens):
+            raise ValueError(f"{nm} must be a float32 [tokens] tensor")
+    if grad is True:
+        grad = torch.empty((tokens, vocab), dtype=logits.dtype, device=logits.device)
+    elif grad is False:
+        grad = None
+    elif grad.dtype != logits.dtype or grad.shape != logits.shape or \
+            (vocab > 1 and grad.stride(1) != 1):
+        raise ValueError("grad must be like logits")
+    ctx, st = _on_device_of(logits, stream, top_logits, top_index, teacher_lse, weight, grad,
+                            loss, lse)
+    if loss is None:
+        loss = torch.empty(tokens, dtype=torch.float32, device=logits.device)
+    if lse is None:
+        lse = torch.empty(tokens, dtype=torch.float32, device=logits.device)
+    # (a single row may report any stride)
+    rows = max(logits.stride(0), vocab) if tokens > 1 else vocab
+    grows = 0 if grad is None else max(grad.stride(0), vocab) if tokens > 1 else vocab
+    if tokens > 1 and (logits.stride(0) < vocab or (grad is not None and grad.stride(0) < vocab)):
+        raise ValueError("rows of logits and grad must not overlap")
+    with ctx:
+        _check(_lib.hqq_distill(_ptr(logits), rows, dt, tokens, vocab, _ptr(top_logits),
+                                _dtype_code(top_logits.dtype, "top_logits"), _ptr(top_index),
+                                top_index.element_size(), top_logits.shape[1],
+                                float(temperature), _ptr(teacher_lse), _ptr(weight), _ptr(loss),
+                                _ptr(lse), _ptr(grad), grows, st))
+    return loss, lse, grad

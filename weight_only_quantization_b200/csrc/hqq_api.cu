@@ -40,6 +40,7 @@ cudaError_t launch_meta_quantize(const __half* x, int64_t n, int log2g, uint8_t*
 cudaError_t launch_meta_dequantize(const uint8_t* codes, const __half* scale, const __half* zero,
                                    int64_t n, int log2g, __half* out, cudaStream_t stream);
 cudaError_t launch_meta_quantize_batch(const MetaJobIn* jobs, int64_t count, cudaStream_t stream);
+cudaError_t launch_distill(const DistillParams& p, int dtype, cudaStream_t stream);
 
 namespace {
 
@@ -502,4 +503,57 @@ extern "C" int hqq_lowrank_noalloc(const void* W, const void* packed, const void
     if (lowrank_scratch(&scratch) != cudaSuccess) return HQQ_ERR_CUDA;
     return hqq_lowrank(W, packed, scale, zero, rows, cols, nbits, group, rank, sketch,
                        power_iters, omega, B, A, sigma, scratch, lowrank_scratch_bytes(), stream);
+}
+
+namespace {
+uintptr_t dtype_bytes(int dtype) { return dtype == HQQ_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == HQQ_F16 || dtype == HQQ_BF16 || dtype == HQQ_F32; }
+}  // namespace
+
+extern "C" int hqq_distill(const void* logits, int64_t logits_stride, int dtype, int64_t tokens,
+                           int64_t vocab, const void* top_logits, int top_dtype,
+                           const void* top_index, int index_bytes, int64_t top_k,
+                           float temperature, const float* teacher_lse, const float* weight,
+                           float* loss, float* lse, void* grad, int64_t grad_stride,
+                           void* stream) {
+    if (tokens < 0 || tokens >= ((int64_t)1 << 27) || vocab < 1 || vocab >= ((int64_t)1 << 31) ||
+        top_k < 1 || top_k > kDistillMaxTop)
+        return HQQ_ERR_SHAPE;
+    if (!dtype_ok(dtype) || !dtype_ok(top_dtype) || (index_bytes != 4 && index_bytes != 8))
+        return HQQ_ERR_UNSUPPORTED;
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+        return HQQ_ERR_PARAM;
+    if (logits_stride < vocab || logits_stride > ((int64_t)1 << 40) ||
+        (grad && (grad_stride < vocab || grad_stride > ((int64_t)1 << 40))))
+        return HQQ_ERR_SHAPE;
+    if (grad == logits && grad && grad_stride != logits_stride) return HQQ_ERR_SHAPE;
+    if (tokens == 0) return HQQ_OK;
+    if (!logits || !top_logits || !top_index) return HQQ_ERR_NULL;
+    if (!aligned(logits, dtype_bytes(dtype)) || !aligned(top_logits, dtype_bytes(top_dtype)) ||
+        !aligned(top_index, (uintptr_t)index_bytes) || (grad && !aligned(grad, dtype_bytes(dtype))) ||
+        (teacher_lse && !aligned(teacher_lse, 4)) || (weight && !aligned(weight, 4)) ||
+        (loss && !aligned(loss, 4)) || (lse && !aligned(lse, 4)))
+        return HQQ_ERR_ALIGN;
+    if (!loss && !lse && !grad) return HQQ_OK;
+    DistillParams p;
+    std::memset(&p, 0, sizeof p);
+    p.logits = logits;
+    p.grad = grad;
+    p.top = top_logits;
+    p.at = top_index;
+    p.teacher_lse = teacher_lse;
+    p.weight = weight;
+    p.loss = loss;
+    p.lse = lse;
+    p.T = tokens;
+    p.V = vocab;
+    p.logits_stride = logits_stride;
+    p.grad_stride = grad_stride;
+    p.K = (int)top_k;
+    p.top_dtype = top_dtype;
+    p.at64 = index_bytes == 8;
+    p.inv_t = 1.0f / temperature;
+    p.log2e_t = (float)(1.4426950408889634 / (double)temperature);
+    const cudaError_t err = launch_distill(p, dtype, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
 }

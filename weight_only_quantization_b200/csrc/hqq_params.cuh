@@ -54,4 +54,21 @@ struct DequantParams {
     Meta8 zq, sq;
 };
 
+// Distillation loss on a teacher's top logits (hqq_distill).  dtypes: 0 fp16,
+// 1 bf16, 2 fp32.
+constexpr int kDistillMaxTop = 1024;
+struct DistillParams {
+    const void* logits;      // [T, V], rows logits_stride elements apart
+    void* grad;              // nullable; the logits' type, rows grad_stride apart
+    const void* top;         // [T, K] teacher logits
+    const void* at;          // [T, K] int32 or int64 (at64) vocabulary indices
+    const float* teacher_lse;  // nullable [T]
+    const float* weight;     // nullable [T]
+    float* loss;             // nullable [T]
+    float* lse;              // nullable [T]
+    int64_t T, V, logits_stride, grad_stride;
+    int K, top_dtype, at64;
+    float inv_t, log2e_t;    // 1 / t and log2(e) / t
+};
+
 }  // namespace hqq
