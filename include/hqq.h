@@ -407,6 +407,88 @@ typedef enum hqq_dtype {
 } hqq_dtype;
 
 /*
+ * Low-rank adapters of many requests beside one quantized matrix: `count` pairs
+ * (A_a, B_a) of one rank, each adding s_a B_a A_a to W_hat for the tokens that
+ * choose it.  hqq_lowrank's residual is one such pair (count 1, fp32).
+ *   A, B     `dtype` [count, rank, cols] and [count, rows, rank], row-major;
+ *            A_stride and B_stride are the elements from one adapter to the next
+ *            (0: dense), aligned to their element.  Adapters of a smaller rank
+ *            are stored with zeros behind it.  16-byte alignment, strides of
+ *            whole 16 bytes and a rank that is a multiple of 8 are fastest.
+ *   scaling  fp32 [count] (s_a), or NULL for 1.
+ *   count    1 .. 65535;  rank 1 .. 512.
+ * A HOST struct of device pointers.
+ */
+typedef struct hqq_adapters {
+    const void* A;
+    const void* B;
+    const float* scaling;
+    int64_t A_stride;
+    int64_t B_stride;
+    int count;
+    int rank;
+    int dtype;               /* hqq_dtype */
+} hqq_adapters;
+
+/*
+ * hqq_linear_adapters_workspace_bytes -- device workspace of hqq_linear_adapters
+ * (backward 0) or hqq_linear_adapters_backward (backward 1) for M tokens on a
+ * [rows, cols] matrix with adapters of this rank and count (rank 0: a backward
+ * call without adapters); -1 for a bad argument.
+ */
+int64_t hqq_linear_adapters_workspace_bytes(int64_t M, int64_t rows, int64_t cols, int rank,
+                                            int count, int backward);
+
+/*
+ * hqq_linear_adapters -- the weight-only linear layer with each token's adapter:
+ *   Y[m, n] = sum_k X[m, k] W_hat[n, k] + s_a sum_j B_a[n, j] sum_k A_a[j, k] X[m, k],
+ * a = index[m].  Both sums are kept in fp32 and Y is rounded once to fp16.
+ *  - A token whose index is negative or not below count has no second term.
+ *  - index NULL: every token has adapter 0.
+ *  - Tokens need no order; a token's result does not depend on the other tokens'
+ *    values or adapters (beyond the summation order of its token count).
+ *   X, M, packed, scale, zero, rows, cols, nbits, group, Y, status  as for
+ *            hqq_linear; zero_q / scale_q (HOST pointers or NULL) replace zero /
+ *            scale by their 8-bit forms as in hqq_linear_meta: exactly one of
+ *            each pair is non-NULL (both: HQQ_ERR_PARAM, neither: HQQ_ERR_NULL).
+ *   adapters [in]  HOST pointer; index [in] int32 [M] or NULL.
+ *   workspace [in] device memory, 256-byte aligned, of at least
+ *            hqq_linear_adapters_workspace_bytes(M, rows, cols, rank, count, 0)
+ *            bytes.  Calls that can overlap on the GPU (other streams, graphs
+ *            replayed side by side) need a workspace each.
+ * Errors: those of hqq_linear, HQQ_ERR_PARAM (rank, count, both of a
+ * pair of zero / scale forms, workspace too small), HQQ_ERR_UNSUPPORTED (dtype).
+ */
+int hqq_linear_adapters(const void* X, int64_t M, const void* packed, const void* scale,
+                        const void* zero, const hqq_meta8* zero_q, const hqq_meta8* scale_q,
+                        int64_t rows, int64_t cols, int nbits, int group,
+                        const hqq_adapters* adapters, const int32_t* index, void* Y, int* status,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * hqq_linear_adapters_backward -- gradients of hqq_linear_adapters for the
+ * gradient dY of its output (the quantized matrix itself is constant):
+ *   dX[m]  = W_hat^T dY[m] + s_a A_a^T (B_a^T dY[m])             fp16 [M, cols]
+ *   dA_a   = s_a sum_{index[m] = a} (B_a^T dY[m]) X[m]^T         fp32 [count, rank, cols]
+ *   dB_a   = s_a sum_{index[m] = a} dY[m] (A_a X[m])^T           fp32 [count, rows, rank]
+ * dA and dB are dense whatever the adapters' strides; an adapter that no token
+ * has gets zeros.  The outputs are overwritten, not added to.  Sums over tokens
+ * run in token order in fp32 (no atomics): the same call gives the same bits.
+ *   dY  [in]  fp16 [M, rows], 16-byte aligned; X [in] fp16 [M, cols], 16-byte
+ *             aligned (NULL allowed without dA and dB).
+ *   dX, dA, dB  [out] each may be NULL to leave it out.
+ *   adapters  NULL: dX = dY W_hat alone (index, X, dA and dB must be NULL).
+ *   workspace as for hqq_linear_adapters, with backward 1.
+ *   other arguments and errors as for hqq_linear_adapters; cols at most 65535 * 128.
+ */
+int hqq_linear_adapters_backward(const void* dY, const void* X, int64_t M, const void* packed,
+                                 const void* scale, const void* zero, const hqq_meta8* zero_q,
+                                 const hqq_meta8* scale_q, int64_t rows, int64_t cols, int nbits,
+                                 int group, const hqq_adapters* adapters, const int32_t* index,
+                                 void* dX, float* dA, float* dB, int* status, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+
+/*
  * hqq_distill -- distillation loss against a teacher's stored top logits, and
  * its gradient with respect to the student's logits.
  *

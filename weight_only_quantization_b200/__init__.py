@@ -17,6 +17,7 @@ __all__ = ["HQQError", "hqq_quantize", "hqq_quantize_ex", "hqq_quantize_half", "
            "Meta8", "hqq_meta_groups", "hqq_meta_quantize", "hqq_meta_quantize_batch",
            "hqq_meta_dequantize",
            "hqq_dequantize_meta", "hqq_linear", "hqq_linear_meta", "hqq_lowrank", "hqq_distill",
+           "Adapters", "hqq_linear_adapters", "hqq_linear_adapters_backward",
            "DEFAULT_P", "DEFAULT_BETA", "DEFAULT_KAPPA", "DEFAULT_ITERS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +79,25 @@ _lib.hqq_lowrank_workspace_bytes.restype = _I64
 _lib.hqq_lowrank.argtypes = [_P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                              _I64, _P]
 _lib.hqq_lowrank.restype = _I
+
+
+class _CAdapters(ctypes.Structure):
+    """struct hqq_adapters of include/hqq.h."""
+    _fields_ = [("A", _P), ("B", _P), ("scaling", _P), ("A_stride", _I64), ("B_stride", _I64),
+                ("count", _I), ("rank", _I), ("dtype", _I)]
+
+
+_lib.hqq_linear_adapters_workspace_bytes.argtypes = [_I64, _I64, _I64, _I, _I, _I]
+_lib.hqq_linear_adapters_workspace_bytes.restype = _I64
+_lib.hqq_linear_adapters.argtypes = [_P, _I64, _P, _P, _P, ctypes.POINTER(_CMeta8),
+                                     ctypes.POINTER(_CMeta8), _I64, _I64, _I, _I,
+                                     ctypes.POINTER(_CAdapters), _P, _P, _P, _P, _I64, _P]
+_lib.hqq_linear_adapters.restype = _I
+_lib.hqq_linear_adapters_backward.argtypes = [_P, _P, _I64, _P, _P, _P, ctypes.POINTER(_CMeta8),
+                                              ctypes.POINTER(_CMeta8), _I64, _I64, _I, _I,
+                                              ctypes.POINTER(_CAdapters), _P, _P, _P, _P, _P, _P,
+                                              _I64, _P]
+_lib.hqq_linear_adapters_backward.restype = _I
 _lib.hqq_distill.argtypes = [_P, _I64, _I, _I64, _I64, _P, _I, _P, _I, _I64, _F, _P, _P, _P, _P,
                              _P, _I64, _P]
 _lib.hqq_distill.restype = _I
@@ -482,3 +502,145 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
                                 float(temperature), _ptr(teacher_lse), _ptr(weight), _ptr(loss),
                                 _ptr(lse), _ptr(grad), grows, st))
     return loss, lse, grad
+
+
+@dataclass
+class Adapters:
+    """Low-rank adapters of one rank beside a quantized matrix: the pair of
+    adapter a adds scaling[a] * B[a] A[a].  A 2-D pair (hqq_lowrank's B and A) is one adapter."""
+    A: "torch.Tensor"          # fp16, bf16 or fp32 [count, rank, cols] (or [rank, cols])
+    B: "torch.Tensor"          # the same type  [count, rows, rank] (or [rows, rank])
+    scaling: "torch.Tensor | None" = None   # fp32 [count]; None: 1
+
+    def _c(self, rows: int, cols: int):
+        A, B = self.A, self.B
+        if A.dim() == 2:
+            A = A.unsqueeze(0)
+        if B.dim() == 2:
+            B = B.unsqueeze(0)
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or \
+                A.shape[1] != B.shape[2] or A.shape[2] != cols or B.shape[1] != rows:
+            raise ValueError("adapters must be A [count, rank, cols] and B [count, rows, rank]")
+        if A.dtype != B.dtype:
+            raise ValueError("A and B must have the same type")
+        count, rank = A.shape[0], A.shape[1]
+        for t, nm in ((A, "A"), (B, "B")):
+            if not t.is_cuda or (t.numel() and not t[0].is_contiguous()):
+                raise ValueError(f"each adapter's {nm} must be a contiguous CUDA matrix")
+            if count > 1 and t.stride(0) < t.shape[1] * t.shape[2]:
+                raise ValueError(f"the adapters of {nm} must not overlap")
+        if self.scaling is not None:
+            _check_tensor(self.scaling, "scaling")
+            import torch
+            if self.scaling.dtype != torch.float32 or self.scaling.numel() != count:
+                raise ValueError("scaling must be a float32 [count] tensor")
+        return _CAdapters(A.data_ptr(), B.data_ptr(),
+                          None if self.scaling is None else self.scaling.data_ptr(),
+                          A.stride(0) if count > 1 else 0, B.stride(0) if count > 1 else 0,
+                          count, rank, _dtype_code(A.dtype, "adapters"))
+
+
+def _adapter_call(x, q, adapters, index, zero_q, scale_q, M, backward, workspace, extra, stream):
+    """What both adapter calls check and marshal."""
+    import torch
+    if index is not None and (index.dtype != torch.int32 or index.numel() != M):
+        raise ValueError("index must be an int32 [M] tensor")
+    for t, nm in ((q.packed, "packed"), (index, "index"), (workspace, "workspace"), *extra):
+        _check_tensor(t, nm)
+    zero = q.zero if zero_q is None else None
+    scale = q.scale if scale_q is None else None
+    for t, nm in ((zero, "zero"), (scale, "scale")):
+        _check_tensor(t, nm)
+    ca = None if adapters is None else adapters._c(q.rows, q.cols)
+    more = [] if adapters is None else [adapters.A, adapters.B, adapters.scaling]
+    for m in (zero_q, scale_q):
+        if m is not None:
+            more += [m.codes, m.scale, m.zero]
+    ctx, st = _on_device_of(x, stream, q.packed, zero, scale, index, workspace,
+                            *more, *(t for t, _ in extra))
+    need = _lib.hqq_linear_adapters_workspace_bytes(M, q.rows, q.cols,
+                                                    0 if ca is None else ca.rank,
+                                                    0 if ca is None else ca.count, backward)
+    if need < 0:
+        raise HQQError(2 if ca is None or (0 < ca.rank <= 512 and 0 < ca.count <= 65535) else 4)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    matrix = (_ptr(q.packed), _ptr(scale), _ptr(zero),
+              None if zero_q is None else ctypes.byref(zero_q._c()),
+              None if scale_q is None else ctypes.byref(scale_q._c()),
+              q.rows, q.cols, q.nbits, q.group, None if ca is None else ctypes.byref(ca))
+    return ctx, st, matrix, workspace, 0 if workspace is None else workspace.numel() * \
+        workspace.element_size()
+
+
+def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, out=None,
+                        status=None, workspace=None, zero_q: Meta8 | None = None,
+                        scale_q: Meta8 | None = None, stream=None):
+    """hqq_linear plus each token's adapter (see include/hqq.h): ``index`` is an
+    int32 [M] tensor (negative or past the last: none), or None for adapter 0
+    everywhere.  ``zero_q`` / ``scale_q`` replace q's zero / scale by their 8-bit
+    form.  The workspace is allocated here unless given."""
+    import torch
+    if X.dtype != torch.float16 or X.dim() != 2 or X.shape[1] != q.cols:
+        raise ValueError("X must be a float16 [M, cols] tensor")
+    M = X.shape[0]
+    if out is None:
+        out = torch.empty((M, q.rows), dtype=torch.float16, device=X.device)
+    elif out.dtype != torch.float16 or out.numel() != M * q.rows:
+        raise ValueError("out must be a float16 [M, rows] tensor")
+    ctx, st, matrix, workspace, nbytes = _adapter_call(
+        X, q, adapters, index, zero_q, scale_q, M, 0, workspace,
+        ((X, "X"), (out, "out"), (status, "status")), stream)
+    with ctx:
+        _check(_lib.hqq_linear_adapters(_ptr(X), M, *matrix, _ptr(index), _ptr(out), _ptr(status),
+                                        _ptr(workspace), nbytes, st))
+    return out
+
+
+def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters | None = None,
+                                 index=None, need_dX: bool = True, need_factors: bool = True,
+                                 dX=None, dA=None, dB=None, status=None, workspace=None,
+                                 zero_q: Meta8 | None = None, scale_q: Meta8 | None = None,
+                                 stream=None):
+    """Gradients (dX, dA, dB) of hqq_linear_adapters for the output's gradient
+    ``dY`` [M, rows] (see include/hqq.h): dX fp16 [M, cols], dA fp32 [count, rank,
+    cols], dB fp32 [count, rows, rank].  Without adapters (X may then be None),
+    or for what need_dX / need_factors leaves out, None is returned in its place."""
+    import torch
+    if dY.dtype != torch.float16 or dY.dim() != 2 or dY.shape[1] != q.rows:
+        raise ValueError("dY must be a float16 [M, rows] tensor")
+    M = dY.shape[0]
+    need_factors = need_factors and adapters is not None
+    if adapters is None and (index is not None or dA is not None or dB is not None):
+        raise ValueError("index, dA and dB need adapters")
+    if not need_factors:
+        X = None
+    elif X is None or X.dtype != torch.float16 or tuple(X.shape) != (M, q.cols):
+        raise ValueError("X must be a float16 [M, cols] tensor")
+    if not need_dX:
+        dX = None
+    elif dX is None:
+        dX = torch.empty((M, q.cols), dtype=torch.float16, device=dY.device)
+    elif dX.dtype != torch.float16 or dX.numel() != M * q.cols:
+        raise ValueError("dX must be a float16 [M, cols] tensor")
+    if need_factors:
+        count = adapters.A.shape[0] if adapters.A.dim() == 3 else 1
+        rank = adapters.A.shape[-2]
+        if dA is None:
+            dA = torch.empty((count, rank, q.cols), dtype=torch.float32, device=dY.device)
+        if dB is None:
+            dB = torch.empty((count, q.rows, rank), dtype=torch.float32, device=dY.device)
+        if dA.dtype != torch.float32 or dA.numel() != count * rank * q.cols or \
+                dB.dtype != torch.float32 or dB.numel() != count * rank * q.rows:
+            raise ValueError("dA and dB must be float32 [count, rank, cols] and "
+                             "[count, rows, rank] tensors")
+    else:
+        dA = dB = None
+    ctx, st, matrix, workspace, nbytes = _adapter_call(
+        dY, q, adapters, index, zero_q, scale_q, M, 1, workspace,
+        ((dY, "dY"), (X, "X"), (dX, "dX"), (dA, "dA"), (dB, "dB"), (status, "status")), stream)
+    with ctx:
+        _check(_lib.hqq_linear_adapters_backward(_ptr(dY), _ptr(X), M, *matrix, _ptr(index),
+                                                 _ptr(dX), _ptr(dA), _ptr(dB), _ptr(status),
+                                                 _ptr(workspace), nbytes, st))
+    return dX, dA, dB

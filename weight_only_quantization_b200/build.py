@@ -17,8 +17,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["hqq_api.cu", "hqq_quantize.cu", "hqq_quantize_half.cu", "hqq_dequantize.cu", "hqq_meta.cu", "hqq_linear.cu", "hqq_decode.cu", "hqq_rtn.cu", "hqq_lowrank.cu",
-           "hqq_distill.cu"]
-HEADERS = ["hqq_common.cuh", "hqq_params.cuh", "hqq_unpack.cuh", "hqq_quantize.cuh"]
+           "hqq_distill.cu", "hqq_adapters.cu", "hqq_linear_adapters.cu",
+           "hqq_linear_backward.cu", "hqq_decode_adapters.cu"]
+HEADERS = ["hqq_common.cuh", "hqq_params.cuh", "hqq_unpack.cuh", "hqq_quantize.cuh",
+           "hqq_linear.cuh", "hqq_decode.cuh", "hqq_lowrank_epi.cuh", "hqq_adapters.cuh"]
 LIB = os.path.join(PKG, "libhqq.so")
 
 COMPILE_FLAGS = [

@@ -6,6 +6,8 @@
 #include <vector>
 
 #include "../../include/hqq.h"
+#include "hqq_adapters.cuh"
+#include "hqq_lowrank_epi.cuh"
 #include "hqq_params.cuh"
 
 namespace hqq {
@@ -41,6 +43,18 @@ cudaError_t launch_meta_dequantize(const uint8_t* codes, const __half* scale, co
                                    int64_t n, int log2g, __half* out, cudaStream_t stream);
 cudaError_t launch_meta_quantize_batch(const MetaJobIn* jobs, int64_t count, cudaStream_t stream);
 cudaError_t launch_distill(const DistillParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_linear_adapters(const LinearParams& prm, const LowRankEpi& lr, const void* X,
+                                   int nbits, cudaStream_t stream);
+cudaError_t launch_decode_adapters(const LinearParams& p, const LowRankEpi& lr, const void* X,
+                                   int nbits, int64_t packed_bytes, cudaStream_t stream);
+cudaError_t launch_linear_backward(const LinearParams& prm, const LowRankEpi& lr, const void* dY,
+                                   int64_t ld, int nbits, cudaStream_t stream);
+cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream);
+cudaError_t launch_order(const int32_t* index, int64_t M, int count, int32_t* order,
+                         int32_t* start, cudaStream_t stream);
+cudaError_t launch_factor_grads(FactorGradParams p, cudaStream_t stream);
+cudaError_t launch_pad_rows(const __half* src, int64_t M, int64_t N, int64_t ld, __half* dst,
+                            cudaStream_t stream);
 
 namespace {
 
@@ -556,4 +570,294 @@ extern "C" int hqq_distill(const void* logits, int64_t logits_stride, int dtype,
     p.log2e_t = (float)(1.4426950408889634 / (double)temperature);
     const cudaError_t err = launch_distill(p, dtype, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int kMaxRank = 512, kMaxAdapters = 65535;
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// The workspace of an adapter call, as byte offsets: T and P (fp32 [M, ld]), the
+// tokens of each adapter (order, start), and dY with padded rows.
+struct AdapterSpace {
+    int64_t T, P, order, start, pad, bytes;
+};
+
+AdapterSpace adapter_space(int64_t M, int64_t rows, int rank, int count, bool backward) {
+    AdapterSpace w;
+    const int64_t mat = round_up(M * round_up(rank, 16) * 4, 256);
+    w.T = 0;
+    w.P = mat;
+    w.order = w.P + (backward ? mat : 0);
+    w.start = w.order + (backward && rank > 0 ? round_up(M * 4, 256) : 0);
+    w.pad = w.start + (backward && rank > 0 ? round_up(((int64_t)count + 1) * 4, 256) : 0);
+    w.bytes = w.pad + (backward && rows % 8 ? round_up(M * round_up(rows, 8) * 2, 256) : 0);
+    return w;
+}
+
+// Checks an adapter struct (its pointers too, unless the call is empty).
+int validate_adapters(const hqq_adapters* a, int64_t rows, int64_t cols, bool pointers) {
+    if (!dtype_ok(a->dtype)) return HQQ_ERR_UNSUPPORTED;
+    if (a->rank < 1 || a->rank > kMaxRank || a->count < 1 || a->count > kMaxAdapters)
+        return HQQ_ERR_PARAM;
+    if (a->A_stride < 0 || a->B_stride < 0 || a->A_stride > ((int64_t)1 << 46) ||
+        a->B_stride > ((int64_t)1 << 46))
+        return HQQ_ERR_SHAPE;
+    if ((a->A_stride && a->A_stride < cols * a->rank) ||
+        (a->B_stride && a->B_stride < rows * a->rank))
+        return HQQ_ERR_SHAPE;
+    if (!pointers) return HQQ_OK;
+    if (!a->A || !a->B) return HQQ_ERR_NULL;
+    if (!aligned(a->A, dtype_bytes(a->dtype)) || !aligned(a->B, dtype_bytes(a->dtype)) ||
+        (a->scaling && !aligned(a->scaling, 4)))
+        return HQQ_ERR_ALIGN;
+    return HQQ_OK;
+}
+
+// The quantized matrix of an adapter call: zero / scale in either form.
+int fill_matrix(LinearParams& prm, const void* packed, const void* scale, const void* zero,
+                const hqq_meta8* zero_q, const hqq_meta8* scale_q, int64_t rows, int64_t cols,
+                int nbits, int group) {
+    int st;
+    if (!packed || (!scale && !scale_q) || (!zero && !zero_q)) return HQQ_ERR_NULL;
+    if (zero_q && (st = meta8_image(zero_q, prm.zq)) != HQQ_OK) return st;
+    if (scale_q && (st = meta8_image(scale_q, prm.sq)) != HQQ_OK) return st;
+    if (!aligned(packed, packed_align(nbits)) || (scale && !aligned(scale, 2)) ||
+        (zero && !aligned(zero, 2)))
+        return HQQ_ERR_ALIGN;
+    prm.packed = static_cast<const uint8_t*>(packed);
+    prm.scale = static_cast<const __half*>(scale);
+    prm.zero = static_cast<const __half*>(zero);
+    prm.N = rows;
+    prm.K = cols;
+    prm.log2_group = log2_of_group(group);
+    return HQQ_OK;
+}
+
+// The checks that both adapter calls share, before pointers.
+int validate_adapter_call(int64_t M, int64_t rows, int64_t cols, int nbits, int group,
+                          const void* scale, const hqq_meta8* scale_q, const void* zero,
+                          const hqq_meta8* zero_q) {
+    const int st = validate_common(rows, cols, nbits, group);
+    if (st != HQQ_OK) return st;
+    if (M < 0 || M > (((int64_t)1 << 31) - 1024)) return HQQ_ERR_SHAPE;
+    if (rows > (int64_t)65535 * 128 || cols > (int64_t)65535 * 128) return HQQ_ERR_SHAPE;
+    if ((scale && scale_q) || (zero && zero_q)) return HQQ_ERR_PARAM;
+    return HQQ_OK;
+}
+
+// An adapter's factor as 16-byte runs of 8 ranks (hqq_lowrank_epi.cuh's vec).
+int rank_runs(const hqq_adapters* a, const void* F, int64_t stride) {
+    return a->dtype != HQQ_F32 && aligned(F, 16) && a->rank % 8 == 0 && stride % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" int64_t hqq_linear_adapters_workspace_bytes(int64_t M, int64_t rows, int64_t cols,
+                                                       int rank, int count, int backward) {
+    if (M < 0 || M > (((int64_t)1 << 31) - 1024) || rows < 0 || rows > (int64_t)65535 * 128 ||
+        cols < 0 || cols > (int64_t)65535 * 128 || rank > kMaxRank || count > kMaxAdapters ||
+        rank < (backward ? 0 : 1) || (rank > 0 && count < 1))
+        return -1;
+    return adapter_space(M, rows, rank, count, backward != 0).bytes;
+}
+
+extern "C" int hqq_linear_adapters(const void* X, int64_t M, const void* packed, const void* scale,
+                                   const void* zero, const hqq_meta8* zero_q,
+                                   const hqq_meta8* scale_q, int64_t rows, int64_t cols, int nbits,
+                                   int group, const hqq_adapters* adapters, const int32_t* index,
+                                   void* Y, int* status, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+    int st = validate_adapter_call(M, rows, cols, nbits, group, scale, scale_q, zero, zero_q);
+    if (st != HQQ_OK) return st;
+    if (!adapters) return HQQ_ERR_NULL;
+    const bool empty = M == 0 || rows == 0 || cols == 0;
+    if ((st = validate_adapters(adapters, rows, cols, !empty)) != HQQ_OK) return st;
+    if (empty) return HQQ_OK;
+    if (!X || !Y || !workspace) return HQQ_ERR_NULL;
+    LinearParams prm;
+    std::memset(&prm, 0, sizeof prm);
+    if ((st = fill_matrix(prm, packed, scale, zero, zero_q, scale_q, rows, cols, nbits, group)) !=
+        HQQ_OK)
+        return st;
+    if (!aligned(X, 16) || !aligned(Y, 2) || (status && !aligned(status, 4)) ||
+        (index && !aligned(index, 4)) || !aligned(workspace, 256))
+        return HQQ_ERR_ALIGN;
+    const AdapterSpace w = adapter_space(M, rows, adapters->rank, adapters->count, false);
+    if (workspace_bytes < w.bytes) return HQQ_ERR_PARAM;
+    prm.Y = static_cast<__half*>(Y);
+    prm.status = status;
+    prm.M = M;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t sA = adapters->A_stride ? adapters->A_stride : cols * adapters->rank;
+    const int64_t sB = adapters->B_stride ? adapters->B_stride : rows * adapters->rank;
+
+    ShrinkParams sh;
+    std::memset(&sh, 0, sizeof sh);
+    sh.X = static_cast<const __half*>(X);
+    sh.F = adapters->A;
+    sh.index = index;
+    sh.scaling = adapters->scaling;
+    sh.T = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.T);
+    sh.M = M;
+    sh.K = sh.ldx = cols;
+    sh.sa = sA;
+    sh.sk = 1;
+    sh.sj = cols;
+    sh.ld = (int)round_up(adapters->rank, 16);
+    sh.rank = adapters->rank;
+    sh.count = adapters->count;
+    sh.dtype = adapters->dtype;
+    if (launch_shrink(sh, s) != cudaSuccess) return HQQ_ERR_CUDA;
+
+    LowRankEpi lr;
+    std::memset(&lr, 0, sizeof lr);
+    lr.T = sh.T;
+    lr.index = index;
+    lr.F = adapters->B;
+    lr.sa = sB;
+    lr.sf = adapters->rank;
+    lr.sj = 1;
+    lr.ld = sh.ld;
+    lr.rank = adapters->rank;
+    lr.count = adapters->count;
+    lr.dtype = adapters->dtype;
+    lr.vec = rank_runs(adapters, adapters->B, sB);
+    const cudaError_t err = M <= decode_max_tokens(nbits)
+        ? launch_decode_adapters(prm, lr, X, nbits, hqq_packed_bytes(rows, cols, nbits), s)
+        : launch_linear_adapters(prm, lr, X, nbits, s);
+    return err == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
+}
+
+extern "C" int hqq_linear_adapters_backward(const void* dY, const void* X, int64_t M,
+                                            const void* packed, const void* scale,
+                                            const void* zero, const hqq_meta8* zero_q,
+                                            const hqq_meta8* scale_q, int64_t rows, int64_t cols,
+                                            int nbits, int group, const hqq_adapters* adapters,
+                                            const int32_t* index, void* dX, float* dA, float* dB,
+                                            int* status, void* workspace, int64_t workspace_bytes,
+                                            void* stream) {
+    int st = validate_adapter_call(M, rows, cols, nbits, group, scale, scale_q, zero, zero_q);
+    if (st != HQQ_OK) return st;
+    if (!adapters && (index || X || dA || dB)) return HQQ_ERR_PARAM;
+    const bool empty = M == 0 || rows == 0 || cols == 0;
+    if (adapters && (st = validate_adapters(adapters, rows, cols, !empty)) != HQQ_OK) return st;
+    if ((dX && !aligned(dX, 2)) || (dA && !aligned(dA, 4)) || (dB && !aligned(dB, 4)))
+        return HQQ_ERR_ALIGN;
+    if (!dX && !dA && !dB) return HQQ_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rank = adapters ? adapters->rank : 0, count = adapters ? adapters->count : 0;
+    if (empty) {                       // sums over nothing
+        if (dX && M && cols && cudaMemsetAsync(dX, 0, (size_t)(M * cols) * 2, s) != cudaSuccess)
+            return HQQ_ERR_CUDA;
+        if (dA && cols &&
+            cudaMemsetAsync(dA, 0, (size_t)count * rank * cols * 4, s) != cudaSuccess)
+            return HQQ_ERR_CUDA;
+        if (dB && rows &&
+            cudaMemsetAsync(dB, 0, (size_t)count * rank * rows * 4, s) != cudaSuccess)
+            return HQQ_ERR_CUDA;
+        return HQQ_OK;
+    }
+    const AdapterSpace w = adapter_space(M, rows, rank, count, true);
+    if (!dY || ((dA || dB) && !X) || (w.bytes > 0 && !workspace)) return HQQ_ERR_NULL;
+    LinearParams prm;
+    std::memset(&prm, 0, sizeof prm);
+    if (dX && (st = fill_matrix(prm, packed, scale, zero, zero_q, scale_q, rows, cols, nbits,
+                                group)) != HQQ_OK)
+        return st;
+    if (!aligned(dY, 16) || (X && !aligned(X, 16)) || (status && !aligned(status, 4)) ||
+        (index && !aligned(index, 4)) || (workspace && !aligned(workspace, 256)))
+        return HQQ_ERR_ALIGN;
+    if (workspace_bytes < w.bytes) return HQQ_ERR_PARAM;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+
+    // rows of dY as whole 16-byte runs
+    const __half* dy = static_cast<const __half*>(dY);
+    const int64_t ldy = round_up(rows, 8);
+    if (ldy != rows) {
+        __half* pad = reinterpret_cast<__half*>(ws + w.pad);
+        if (launch_pad_rows(dy, M, rows, ldy, pad, s) != cudaSuccess) return HQQ_ERR_CUDA;
+        dy = pad;
+    }
+    LowRankEpi lr;
+    std::memset(&lr, 0, sizeof lr);
+    if (adapters) {
+        const int64_t sA = adapters->A_stride ? adapters->A_stride : cols * rank;
+        const int64_t sB = adapters->B_stride ? adapters->B_stride : rows * rank;
+        ShrinkParams sh;
+        std::memset(&sh, 0, sizeof sh);
+        sh.index = index;
+        sh.scaling = adapters->scaling;
+        sh.M = M;
+        sh.ld = (int)round_up(rank, 16);
+        sh.rank = rank;
+        sh.count = count;
+        sh.dtype = adapters->dtype;
+        float* T = reinterpret_cast<float*>(ws + w.T);
+        float* P = reinterpret_cast<float*>(ws + w.P);
+        if (dB) {                      // T = s X A^T
+            sh.X = static_cast<const __half*>(X);
+            sh.F = adapters->A;
+            sh.T = T;
+            sh.K = sh.ldx = cols;
+            sh.sa = sA;
+            sh.sk = 1;
+            sh.sj = cols;
+            if (launch_shrink(sh, s) != cudaSuccess) return HQQ_ERR_CUDA;
+        }
+        if (dA || dX) {                // P = s dY B
+            sh.X = dy;
+            sh.F = adapters->B;
+            sh.T = P;
+            sh.K = rows;
+            sh.ldx = ldy;
+            sh.sa = sB;
+            sh.sk = rank;
+            sh.sj = 1;
+            if (launch_shrink(sh, s) != cudaSuccess) return HQQ_ERR_CUDA;
+        }
+        if (dA || dB) {
+            FactorGradParams fg;
+            std::memset(&fg, 0, sizeof fg);
+            if (index) {
+                int32_t* order = reinterpret_cast<int32_t*>(ws + w.order);
+                int32_t* start = reinterpret_cast<int32_t*>(ws + w.start);
+                if (launch_order(index, M, count, order, start, s) != cudaSuccess)
+                    return HQQ_ERR_CUDA;
+                fg.order = order;
+                fg.start = start;
+            }
+            fg.X = static_cast<const __half*>(X);
+            fg.dY = dy;
+            fg.P = P;
+            fg.T = T;
+            fg.dA = dA;
+            fg.dB = dB;
+            fg.M = M;
+            fg.N = rows;
+            fg.K = fg.ldx = cols;
+            fg.ldy = ldy;
+            fg.ld = sh.ld;
+            fg.rank = rank;
+            fg.count = count;
+            if (launch_factor_grads(fg, s) != cudaSuccess) return HQQ_ERR_CUDA;
+        }
+        lr.T = P;
+        lr.index = index;
+        lr.F = adapters->A;
+        lr.sa = sA;
+        lr.sf = 1;
+        lr.sj = cols;
+        lr.ld = sh.ld;
+        lr.rank = rank;
+        lr.count = count;
+        lr.dtype = adapters->dtype;
+    }
+    if (!dX) return HQQ_OK;
+    prm.Y = static_cast<__half*>(dX);
+    prm.status = status;
+    prm.M = M;
+    return launch_linear_backward(prm, lr, dy, ldy, nbits, s) == cudaSuccess ? HQQ_OK
+                                                                             : HQQ_ERR_CUDA;
 }
