@@ -24,6 +24,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "hqq_params.cuh"
 
 namespace cg = cooperative_groups;
@@ -88,57 +90,74 @@ __device__ __forceinline__ Pack<T, W> row_pack(const T* row, int64_t i, int64_t 
     return r;
 }
 
-// (maximum, sum of exp relative to it) of two parts; a part without finite
-// values has maximum -inf and sum 0 (or NaN, which is kept).
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
-    const float mm = fmaxf(m, m2);
-    if (mm == -INFINITY) {
-        s = __fadd_rn(s, s2);
-    } else {
-        s = __fmaf_rn(s, ex2(__fmul_rn(__fsub_rn(m, mm), c)),
-                      __fmul_rn(s2, ex2(__fmul_rn(__fsub_rn(m2, mm), c))));
-        m = mm;
-    }
+// The joined (maximum, sum of exponentials relative to it) of the warp's lanes,
+// in a fixed order; lanes without values hold (-inf, 0).  A maximum of -inf
+// keeps the plain sum (0, or the NaN of a value).
+template <int LANES>
+__device__ __forceinline__ void join_lanes(float& m, float& s, float c) {
+    float mm = m;
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    s = __fmul_rn(s, mm == -INFINITY ? 1.0f : ex2(__fmul_rn(__fsub_rn(m, mm), c)));
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+    m = mm;
 }
 
-// The exponentials of a pack relative to m, times 1: e[i] = 2^((z_i - m) c).
+// The exponentials of a pack relative to m: e[i] = 2^((z_i - m) c).
 template <typename T, int W>
-__device__ __forceinline__ void exps(const Pack<T, W>& z, float m, float c, float (&e)[W]) {
+__device__ __forceinline__ void exps(const Pack<T, W>& z, float m, float c, float2 (&e)[(W + 1) / 2]) {
     if constexpr (W == 1) {
-        e[0] = ex2(__fmul_rn(__fsub_rn(as_float(z.v[0]), m), c));
+        e[0].x = ex2(__fmul_rn(__fsub_rn(as_float(z.v[0]), m), c));
+        e[0].y = 0.0f;
     } else {
 #pragma unroll
         for (int i = 0; i < W; i += 2) {
             const float2 d = __fmul2_rn(
                 __fadd2_rn(make_float2(as_float(z.v[i]), as_float(z.v[i + 1])), make_float2(-m, -m)),
                 make_float2(c, c));
-            e[i] = ex2(d.x);
-            e[i + 1] = ex2(d.y);
+            e[i / 2] = make_float2(ex2(d.x), ex2(d.y));
         }
     }
 }
 
-// Running maximum and sum of a thread, a pack further.
+// The largest value of N packs (NaN is passed over: it shows in the sum).
+template <typename T, int W, int N>
+__device__ __forceinline__ float pack_max(const Pack<T, W> (&z)[N]) {
+    if constexpr (W == 1 || sizeof(T) == 4) {
+        float mx = as_float(z[0].v[0]);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int e = 0; e < W; ++e) mx = fmaxf(mx, as_float(z[u].v[e]));
+        return mx;
+    } else {                                             // two 16-bit values an operation
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                             __nv_bfloat162>::type;
+        T2 mx = *reinterpret_cast<const T2*>(&z[0].v[0]);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int e = 0; e < W; e += 2)
+                mx = __hmax2(mx, *reinterpret_cast<const T2*>(&z[u].v[e]));
+        return fmaxf(as_float(mx.x), as_float(mx.y));
+    }
+}
+
+// Running maximum and sum of a thread, N packs further.
 template <typename T, int W, int N>
 __device__ __forceinline__ void local_stats(const Pack<T, W> (&z)[N], float c, float& m, float& s) {
-    float mx = m;
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-#pragma unroll
-        for (int e = 0; e < W; ++e) mx = fmaxf(mx, as_float(z[u].v[e]));
+    const float mx = fmaxf(m, pack_max(z));
     const float base = mx == -INFINITY ? 0.0f : mx;
-    float a = 0.0f, b = 0.0f;
+    float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-        float e[W];
+        float2 e[(W + 1) / 2];
         exps(z[u], base, c, e);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i & 1) b = __fadd_rn(b, e[i]);
-            else a = __fadd_rn(a, e[i]);
-        }
+        for (int i = 0; i < (W + 1) / 2; ++i) acc = __fadd2_rn(acc, e[i]);
     }
-    const float sum = __fadd_rn(a, b);
+    const float sum = __fadd_rn(acc.x, acc.y);
     // what came before (m, s), relative to the new maximum
     s = m == -INFINITY ? __fadd_rn(s, sum)
                        : __fmaf_rn(s, ex2(__fmul_rn(__fsub_rn(m, base), c)), sum);
@@ -159,22 +178,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
 // Grid: one cluster of `csize` CTAs per token.  CACHED: the CTA's share of the
 // row is at most kDsThreads * NV packs and stays in registers.
 template <typename T, int W, int NV, bool CACHED>
 __global__ void __launch_bounds__(kDsThreads, 2)
 distill_kernel(const __grid_constant__ DistillParams p, int csize) {
-    __shared__ float sp[kDistillMaxTop], sz[kDistillMaxTop];
-    __shared__ int si[kDistillMaxTop];
-    __shared__ float wm[kDsWarps], ws[kDsWarps];
+    __shared__ float st[kDistillMaxTop], sz[kDistillMaxTop];   // teacher value, student logit
+    __shared__ int4 si4[kDistillMaxTop / 4];                   // index, or -1
+    __shared__ float wm[kDsWarps], ws[kDsWarps], tm_w[kDsWarps], ts_w[kDsWarps], loss_w[kDsWarps];
     __shared__ float cm[kDsMaxCluster], cs[kDsMaxCluster];
-    __shared__ float psum_s, norm_s;
+    int* si = reinterpret_cast<int*>(si4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = csize == 1 ? 0 : (int)(blockIdx.x % (unsigned)csize);
@@ -207,11 +220,10 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
     Pack<T, W> z[NV];
-    float m = -INFINITY, s = 0.0f;
-    if constexpr (CACHED) {
+    auto load_round = [&](int64_t i0) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            const int64_t i = lo + tid + (int64_t)u * kDsThreads;
+            const int64_t i = i0 + (int64_t)u * kDsThreads;
             if (i < hi) {
                 z[u] = row_pack<T, W>(row, i, p.V);
             } else {
@@ -219,82 +231,55 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
                 for (int e = 0; e < W; ++e) z[u].v[e] = from_float<T>(-INFINITY);
             }
         }
-    }
+    };
+    if constexpr (CACHED) load_round(lo + tid);          // in flight behind the entries' loads
 
-    // ---- the teacher's entries: p_k, and the student's logit at each index
-    // (rank 0 needs all of them for the loss, the others their own segment's)
-    if (warp == kDsWarps - 1) {
-        const int64_t seg0 = lo * W, seg1 = hi * W;
-        float peak = -INFINITY;
-        for (int k = lane; k < p.K; k += 32) {
-            const int64_t at = p.at64 ? static_cast<const int64_t*>(p.at)[tok * p.K + k]
-                                      : (int64_t) static_cast<const int32_t*>(p.at)[tok * p.K + k];
-            const bool ok = at >= 0 && at < p.V;
-            const float t = ok ? load_top(p, tok * p.K + k) : -INFINITY;
-            si[k] = ok ? (int)at : -1;
-            sp[k] = t;
-            sz[k] = ok && (rank == 0 || (at >= seg0 && at < seg1)) ? as_float(row[at]) : 0.0f;
-            peak = fmaxf(peak, t);
-        }
-        peak = warp_max(peak);
-        float total = 0.0f;
-        if (p.teacher_lse == nullptr) {
-            for (int k = lane; k < p.K; k += 32) {
-                const float t = sp[k];
-                if (t != -INFINITY) total = __fadd_rn(total, expf(__fmul_rn(__fsub_rn(t, peak), p.inv_t)));
-            }
-            total = warp_sum(total);
-        }
-        const float norm = p.teacher_lse ? p.teacher_lse[tok] : logf(total);
-        float ps = 0.0f;
-        for (int k = lane; k < p.K; k += 32) {
-            const float t = sp[k];
-            const float lp = p.teacher_lse ? __fsub_rn(__fmul_rn(t, p.inv_t), norm)
-                                           : __fsub_rn(__fmul_rn(__fsub_rn(t, peak), p.inv_t), norm);
-            // entries without mass (unused, or a value of -inf) take no part
-            const float pk = si[k] < 0 || t == -INFINITY ? 0.0f : expf(lp);
-            sp[k] = pk;
-            ps = __fadd_rn(ps, pk);
-        }
-        ps = warp_sum(ps);
-        if (lane == 0) {
-            psum_s = ps;
-            norm_s = p.teacher_lse ? norm : __fadd_rn(norm, __fmul_rn(peak, p.inv_t));
-        }
+    // ---- the teacher's entries, one a thread (two from 512 entries on): value,
+    // index and the student's logit there (rank 0 needs all of them for the loss,
+    // the others their own segment's), (maximum, sum) as for the row
+    const int64_t seg0 = lo * W, seg1 = hi * W;
+    float tm = -INFINITY, ts = 0.0f;
+    for (int k = tid; k < p.K; k += kDsThreads) {
+        const int64_t at = p.at64 ? static_cast<const int64_t*>(p.at)[tok * p.K + k]
+                                  : (int64_t) static_cast<const int32_t*>(p.at)[tok * p.K + k];
+        const float t0 = load_top(p, tok * p.K + k);
+        const bool ok = at >= 0 && at < p.V;
+        const float t = ok ? t0 : -INFINITY;
+        si[k] = ok ? (int)at : -1;
+        st[k] = t;
+        sz[k] = ok && (rank == 0 || (at >= seg0 && at < seg1)) ? as_float(row[at]) : 0.0f;
+        const float mx = fmaxf(tm, t), base = mx == -INFINITY ? 0.0f : mx;
+        ts = __fadd_rn(__fmul_rn(ts, tm == -INFINITY ? 1.0f : ex2(__fmul_rn(__fsub_rn(tm, base), c))),
+                       ex2(__fmul_rn(__fsub_rn(t, base), c)));
+        tm = mx;
     }
+    if (tid < 4 && p.K + tid < ((p.K + 3) & ~3)) si[p.K + tid] = -1;   // the last int4
 
     // ---- maximum and sum of exponentials of the row
+    float m = -INFINITY, s = 0.0f;
     if constexpr (CACHED) {
         local_stats(z, c, m, s);
     } else {
         for (int64_t i0 = lo + tid; i0 < hi; i0 += (int64_t)NV * kDsThreads) {
-#pragma unroll
-            for (int u = 0; u < NV; ++u) {
-                const int64_t i = i0 + (int64_t)u * kDsThreads;
-                if (i < hi) {
-                    z[u] = row_pack<T, W>(row, i, p.V);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < W; ++e) z[u].v[e] = from_float<T>(-INFINITY);
-                }
-            }
+            load_round(i0);
             local_stats(z, c, m, s);
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        join(m, s, m2, s2, c);
-    }
+    join_lanes<32>(m, s, c);
+    if (warp * 32 < p.K) join_lanes<32>(tm, ts, c);
     if (lane == 0) {
         wm[warp] = m;
         ws[warp] = s;
+        tm_w[warp] = tm;                                 // (-inf, 0) where there are no entries
+        ts_w[warp] = ts;
     }
     __syncthreads();
-    m = wm[0];
-    s = ws[0];
-#pragma unroll
-    for (int i = 1; i < kDsWarps; ++i) join(m, s, wm[i], ws[i], c);
+    m = wm[lane % kDsWarps];
+    s = ws[lane % kDsWarps];
+    tm = tm_w[lane % kDsWarps];
+    ts = ts_w[lane % kDsWarps];
+    join_lanes<kDsWarps>(m, s, c);
+    join_lanes<kDsWarps>(tm, ts, c);
     if (csize > 1) {
         cg::cluster_group cluster = cg::this_cluster();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -304,72 +289,101 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
         }
         asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        m = cm[0];
-        s = cs[0];
-        for (int i = 1; i < csize; ++i) join(m, s, cm[i], cs[i], c);
+        m = lane % kDsMaxCluster < csize ? cm[lane % kDsMaxCluster] : -INFINITY;
+        s = lane % kDsMaxCluster < csize ? cs[lane % kDsMaxCluster] : 0.0f;
+        join_lanes<kDsMaxCluster>(m, s, c);
     }
-    const float psum = psum_s;
     const float logs = logf(s);
+    // L, log p_k = t_k / t - L and sum of the p_k (1 up to rounding without a
+    // teacher_lse); no entry, or none with mass: L = -inf, sum 0
+    const bool given = p.teacher_lse != nullptr;
+    const float L = given ? p.teacher_lse[tok] : logf(ts);
+    const float toff = given || tm == -INFINITY ? 0.0f : tm;
+    auto log_p = [&](float t) { return __fsub_rn(__fmul_rn(__fsub_rn(t, toff), p.inv_t), L); };
+    const float psum = tm == -INFINITY ? __fmul_rn(ts, 0.0f)
+                       : given ? __fmul_rn(ts, expf(__fsub_rn(__fmul_rn(tm, p.inv_t), L)))
+                               : __fdiv_rn(ts, ts);
 
     // ---- loss (rank 0)
     if (rank == 0 && p.lse && tid == 0) p.lse[tok] = __fadd_rn(__fmul_rn(m, p.inv_t), logs);
-    if (rank == 0 && p.loss && warp == 0) {
+    if (rank == 0 && p.loss && warp * 32 < p.K) {
         float acc = 0.0f;
-        for (int k = lane; k < p.K; k += 32) {
-            const float pk = sp[k];
+        for (int k = tid; k < p.K; k += kDsThreads) {
+            const float t = st[k];
+            // entries without mass (unused, or a value of -inf) take no part
+            const float lp = log_p(t), pk = t == -INFINITY ? 0.0f : expf(lp);
             if (pk != 0.0f) {                            // (NaN != 0: kept)
-                const float lp = __fsub_rn(__fmul_rn(load_top(p, tok * p.K + k), p.inv_t), norm_s);
                 const float lq = __fsub_rn(__fmul_rn(__fsub_rn(sz[k], m), p.inv_t), logs);
                 acc = __fmaf_rn(pk, __fsub_rn(lp, lq), acc);
             }
         }
         acc = warp_sum(acc);
-        if (lane == 0) p.loss[tok] = __fmul_rn(w, acc);
+        if (lane == 0) loss_w[warp] = acc;
     }
-    if (!grow) return;
 
     // ---- gradient: the dense row, then the entries' places
     const float wt = __fmul_rn(w, p.inv_t);
-    const float coef = __fdiv_rn(__fmul_rn(wt, psum), s);
-    for (int64_t i0 = lo + tid; i0 < hi; i0 += (int64_t)NV * kDsThreads) {
+    if (grow) {
+        const float coef = __fdiv_rn(__fmul_rn(wt, psum), s);
+        for (int64_t i0 = lo + tid; i0 < hi; i0 += (int64_t)NV * kDsThreads) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int64_t i = i0 + (int64_t)u * kDsThreads;
-            if (i < hi) {
-                Pack<T, W> q;
-                float e[W];
-                if constexpr (CACHED) q = z[u];
-                else q = row_pack<T, W>(row, i, p.V);
-                exps(q, m, c, e);
+            for (int u = 0; u < NV; ++u) {
+                const int64_t i = i0 + (int64_t)u * kDsThreads;
+                if (i < hi) {
+                    Pack<T, W> q;
+                    float2 e[(W + 1) / 2];
+                    if constexpr (CACHED) q = z[u];
+                    else q = row_pack<T, W>(row, i, p.V);
+                    exps(q, m, c, e);
 #pragma unroll
-                for (int j = 0; j < W; ++j) q.v[j] = from_float<T>(__fmul_rn(e[j], coef));
-                if (W == 1 || (i + 1) * W <= p.V) {
-                    store_pack<T, W>(grow + i * W, q);
-                } else {
+                    for (int j = 0; j < (W + 1) / 2; ++j) {
+                        e[j] = __fmul2_rn(e[j], make_float2(coef, coef));
+                        q.v[2 * j] = from_float<T>(e[j].x);
+                        if constexpr (W > 1) q.v[2 * j + 1] = from_float<T>(e[j].y);
+                    }
+                    if (W == 1 || (i + 1) * W <= p.V) {
+                        store_pack<T, W>(grow + i * W, q);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (i * W + j < p.V) grow[i * W + j] = q.v[j];
+                        for (int j = 0; j < W; ++j)
+                            if (i * W + j < p.V) grow[i * W + j] = q.v[j];
+                    }
                 }
             }
+            if constexpr (CACHED) break;
         }
-        if constexpr (CACHED) break;                     // one round holds the whole share
     }
     __syncthreads();                                     // the dense row is stored
-    const int64_t seg0 = lo * W, seg1 = hi * W;
+    if (rank == 0 && p.loss && tid == 0) {
+        float acc = loss_w[0];
+        for (int i = 1; i * 32 < p.K && i < kDsWarps; ++i) acc = __fadd_rn(acc, loss_w[i]);
+        p.loss[tok] = __fmul_rn(w, acc);
+    }
+    if (!grow) return;
+    const float coef = __fdiv_rn(__fmul_rn(wt, psum), s);
+    auto mass_of = [&](int k) { return st[k] == -INFINITY ? 0.0f : expf(log_p(st[k])); };
     for (int k = tid; k < p.K; k += kDsThreads) {
         const int at = si[k];
         if (at < seg0 || at >= seg1) continue;           // (unused entries: -1)
-        bool first = true;
-        float mass = 0.0f;
-        for (int j = 0; j < p.K; ++j)
-            if (si[j] == at) {
-                if (j < k) first = false;
-                mass = __fadd_rn(mass, sp[j]);
-            }
-        if (first) {
-            const float e = ex2(__fmul_rn(__fsub_rn(sz[k], m), c));
-            grow[at] = from_float<T>(__fmaf_rn(e, coef, -__fmul_rn(wt, mass)));
+        int same = 0;                                    // entries of this index
+#pragma unroll 4
+        for (int j = 0; j < (p.K + 3) / 4; ++j) {
+            const int4 o = si4[j];
+            same += (o.x == at) + (o.y == at) + (o.z == at) + (o.w == at);
         }
+        float mass = mass_of(k);
+        if (same > 1) {                                  // in entry order; the first writes
+            bool first = true;
+            mass = 0.0f;
+            for (int j = 0; j < p.K; ++j)
+                if (si[j] == at) {
+                    if (j < k) first = false;
+                    mass = __fadd_rn(mass, mass_of(j));
+                }
+            if (!first) continue;
+        }
+        const float e = ex2(__fmul_rn(__fsub_rn(sz[k], m), c));
+        grow[at] = from_float<T>(__fmaf_rn(e, coef, -__fmul_rn(wt, mass)));
     }
 }
 
