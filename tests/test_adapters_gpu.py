@@ -522,3 +522,36 @@ def test_distilled_step(hqq):
     for x, w, nm in zip((dX, dA, dB), backward_ref(dlogits.cpu(), h, W, ad, index), "XAB"):
         close(x, w, "d" + nm)
     close(after, forward_ref(h, W, step, index), "after")
+
+
+@pytest.mark.parametrize("rows,cols,M", [(3200, 2048, 300), (3200, 2064, 777), (4103, 1024, 2048),
+                                         (2176, 8192, 1030), (1024, 4112, 129)])
+@pytest.mark.parametrize("nbits", [3, 4])
+def test_large_tiles_exact(hqq, rows, cols, M, nbits):
+    """Token tiles of up to 512, pairs of CTAs, reductions split over a cluster
+    and their combinations, bit for bit on small integers."""
+    count, rank = 3, 8
+    q, W = matrix(hqq, rows, cols, nbits, 16, seed=M, integer=True)
+    g = torch.Generator().manual_seed(M)
+    A = torch.randint(-1, 2, (count, rank, cols), generator=g).half()
+    B = torch.randint(-1, 2, (count, rows, rank), generator=g).half()
+    ad = hqq.Adapters(A.cuda(), B.cuda(), torch.tensor([1.0, 2.0, -1.0]).cuda())
+    index = indices(M, count, "mixed" if nbits == 3 else "runs", M)
+    X = torch.randint(-1, 2, (M, cols), generator=g).half()
+    dY = torch.randint(-1, 2, (M, rows), generator=g).half()
+    Y = hqq.hqq_linear_adapters(X.cuda(), q, ad, index.cuda())
+    got = hqq.hqq_linear_adapters_backward(dY.cuda(), X.cuda(), q, ad, index.cuda())
+    on = (index >= 0) & (index < count)
+    i = torch.where(on, index, 0).long()
+    s = ad.scaling.cpu().double()[i] * on
+    x, y, w = X.double().cuda(), dY.double().cuda(), W.cuda()
+    hot = (torch.nn.functional.one_hot(i, count) * s[:, None]).cuda()
+    T = torch.einsum("mk,ajk,ma->maj", x, A.double().cuda(), hot)
+    P = torch.einsum("mn,anj,ma->maj", y, B.double().cuda(), hot)
+    want = x @ w.T + torch.einsum("maj,anj->mn", T, B.double().cuda())
+    assert float(want.abs().max()) < 65504 and torch.equal(Y, want.half())
+    want = y @ w + torch.einsum("maj,ajk->mk", P, A.double().cuda())
+    assert float(want.abs().max()) < 65504 and torch.equal(got[0], want.half())
+    dA, dB = torch.einsum("maj,mk->ajk", P, x), torch.einsum("maj,mn->anj", T, y)
+    assert max(float(dA.abs().max()), float(dB.abs().max())) < 2 ** 24
+    assert torch.equal(got[1], dA.float()) and torch.equal(got[2], dB.float())

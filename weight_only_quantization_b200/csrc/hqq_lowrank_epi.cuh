@@ -79,55 +79,105 @@ __device__ __forceinline__ float lowrank_dot16(const float* t, const float2 (&b)
     return __fadd_rn(acc.x, acc.y);
 }
 
-// The 16 factor values that a thread holds from one token to the next.
-struct LowRankRegs {
-    float2 b[8];
+// The factor values of up to 32 ranks that a thread holds from one token to the
+// next: adapter a, ranks from j0.
+struct LowRankRegs32 {
+    float2 b[2][8];
     int a, j0;
     __device__ __forceinline__ void init() { a = -1; j0 = 0; }
-    __device__ __forceinline__ void want(const LowRankEpi& e, int adapter, int64_t f, int j) {
-        if (adapter != a || j != j0) {
-            lowrank_load16(e, adapter, f, j, b);
-            a = adapter;
-            j0 = j;
-        }
-    }
 };
 
-// v[i] += the term of token m + i (i < 8) at the thread's feature f.  Every
-// lane of the warp has the same tokens.
-__device__ __forceinline__ void lowrank_add8(const LowRankEpi& e, LowRankRegs& r, int64_t m,
-                                             int64_t M, int64_t f, float (&v)[8]) {
-    int a[8];
-    bool same = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a[i] = m + i < M ? lowrank_adapter(e, m + i) : -1;
-        same = same && a[i] == a[0];
+// A tile's rows of T and its tokens' adapters in shared memory (T stays in global
+// memory where the room is too small for it).
+struct LowRankTile {
+    int* adapter;
+    float* rows;
+    uint32_t room;           // bytes for rows
+    const float* t;          // row 0 of the staged tokens
+    __device__ __forceinline__ void place(uint8_t* mem, uint32_t bytes) {
+        adapter = reinterpret_cast<int*>(mem);           // 16-byte aligned
+        rows = reinterpret_cast<float*>(mem + 2048);     // up to 512 tokens
+        room = bytes - 2048u;
+        t = nullptr;
     }
-    if (same) {
-        if (a[0] < 0) return;
-        for (int j = 0; j < e.ld; j += 16) {
-            r.want(e, a[0], f, j);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = __fadd_rn(v[i], lowrank_dot16(e.T + (m + i) * e.ld + j, r.b));
+    // tokens m .. m + n - 1 (those past M have none), by all `nt` threads of the
+    // CTA; the caller synchronises before add8
+    __device__ __forceinline__ void stage(const LowRankEpi& e, int64_t m, int n, int64_t M, int tid,
+                                          int nt) {
+        for (int i = tid; i < n; i += nt) adapter[i] = m + i < M ? lowrank_adapter(e, m + i) : -1;
+        const int per = e.ld >> 2;                       // float4s a row
+        t = e.T + m * e.ld;
+        if ((uint32_t)(n * e.ld) * 4u <= room) {
+            const int64_t have = (M - m) * per;
+            const int all = n * per < have ? n * per : (int)have;
+            for (int i = tid; i < all; i += nt)
+                reinterpret_cast<float4*>(rows)[i] = __ldg(reinterpret_cast<const float4*>(t) + i);
+            t = rows;
         }
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            if (m + i >= M) break;
-            const int ai = lowrank_adapter(e, m + i);
-            if (ai < 0) continue;
-            float d = 0.0f;
-            for (int j = 0; j < e.ld; j += 16) {
-                r.want(e, ai, f, j);
-                d = __fadd_rn(d, lowrank_dot16(e.T + (m + i) * e.ld + j, r.b));
+    }
+    // sum of 16 products of the staged token i from rank j (the same for the warp)
+    __device__ __forceinline__ float dot16(const LowRankEpi& e, int i, int j,
+                                           const float2 (&b)[8]) const {
+        const float4* row = reinterpret_cast<const float4*>(t + (int64_t)i * e.ld + j);
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 x = row[q];
+            acc = __ffma2_rn(make_float2(x.x, x.y), b[2 * q], acc);
+            acc = __ffma2_rn(make_float2(x.z, x.w), b[2 * q + 1], acc);
+        }
+        return __fadd_rn(acc.x, acc.y);
+    }
+    // v[i] += the term of staged token c + i (i < 8) at feature f
+    __device__ __forceinline__ void add8(const LowRankEpi& e, LowRankRegs32& r, int c, int64_t f,
+                                         float (&v)[8]) const {
+        const int4 a0 = *reinterpret_cast<const int4*>(adapter + c);
+        const int4 a1 = *reinterpret_cast<const int4*>(adapter + c + 4);
+        const bool same = a0.y == a0.x && a0.z == a0.x && a0.w == a0.x && a1.x == a0.x &&
+                          a1.y == a0.x && a1.z == a0.x && a1.w == a0.x;
+        if (same) {
+            if (a0.x < 0) return;
+            for (int j = 0; j < e.ld; j += 32) {
+                const bool two = j + 16 < e.ld;
+                if (r.a != a0.x || r.j0 != j) {
+                    lowrank_load16(e, a0.x, f, j, r.b[0]);
+                    if (two) lowrank_load16(e, a0.x, f, j + 16, r.b[1]);
+                    r.a = a0.x;
+                    r.j0 = j;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = __fadd_rn(v[i], dot16(e, c + i, j, r.b[0]));
+                    if (two) v[i] = __fadd_rn(v[i], dot16(e, c + i, j + 16, r.b[1]));
+                }
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = k == i ? __fadd_rn(v[k], d) : v[k];
+            return;
         }
+        // tokens of several adapters: 16 ranks of one token a step, the next
+        // step's factor values loaded ahead
+        const int steps = e.ld >> 4, all = 8 * steps;
+        auto adapter_of = [&](int q) { return adapter[c + q / steps]; };
+        auto load = [&](int q, float2 (&b)[8]) {
+            if (q < all && adapter_of(q) >= 0)
+                lowrank_load16(e, adapter_of(q), f, 16 * (q % steps), b);
+        };
+        auto add = [&](int q, const float2 (&b)[8]) {
+            if (q >= all || adapter_of(q) < 0) return;
+            const float d = dot16(e, c + q / steps, 16 * (q % steps), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i == q / steps ? __fadd_rn(v[i], d) : v[i];
+        };
+        load(0, r.b[0]);
+#pragma unroll 1
+        for (int q = 0; q < all; q += 2) {
+            load(q + 1, r.b[1]);
+            add(q, r.b[0]);
+            load(q + 2, r.b[0]);
+            add(q + 1, r.b[1]);
+        }
+        r.a = -1;
     }
-}
+};
 
 // The term of one (token, feature), for kernels whose lanes hold different
 // tokens.
