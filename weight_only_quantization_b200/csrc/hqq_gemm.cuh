@@ -8,7 +8,7 @@
 // the output.  Tensor cores: tcgen05.mma kind::f16, fp32 accumulators in tensor
 // memory, the output transposed (features x tokens):
 //   A = 128 features x 64 of the reduction, written to shared memory by 16
-//       producer warps that unpack 16 codes a thread.  Layer: K-major.  Gradient
+//       producer warps that unpack 64 codes a thread.  Layer: K-major.  Gradient
 //       (TRANS): the same packed rows read as [64 n][128 k] and stored
 //       k-contiguous (MN-major); the transposition is the MMA descriptor's.
 //   B = bn tokens x 64 of the reduction by TMA.
@@ -39,20 +39,21 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kGmThreads = 576;
-constexpr int kGmProducers = 16;                 // warps
+constexpr int kGmGroups = 4;                     // producer groups of four warps
 constexpr int kGmM = 128;                        // features per CTA
 constexpr int kGmK = 64;                         // reduction per stage
 constexpr uint32_t kGmABytes = kGmM * kGmK * 2;
 constexpr uint32_t kGmStageBytes = 196608;       // all stages together (192 KiB)
 constexpr int kGmMaxStages = 8;
+constexpr int kGmTries = 1000;                   // of a wait before it is timed (bounded)
 constexpr int kGmWindow = 256;                   // tokens whose partial sums travel at once
-constexpr int kGmAhead = 4;                      // reduction steps of codes in registers
 
 struct GemmShape {
     int bn;                  // tokens per tile
     int nmma;                // tokens per MMA (bn, or bn / 2 above 256)
     int stages, ks;
     uint32_t b_bytes;        // staged tokens of a CTA: bn / CG rows of 128 bytes
+    int vec;                 // 32 codes are one aligned run in memory (4 bits)
 };
 
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
@@ -135,82 +136,145 @@ __device__ __forceinline__ void gemm_commit(uint32_t bar, uint16_t pair) {
             : "memory");
 }
 
-// 16 consecutive codes of one row (inside one group; rows are whole runs of 16)
-// as loaded, with their (scale, zero).  Absent ones decode to 0.
+// Read-only loads that stay where they are written (plain ones may be moved down
+// to their use a step later).
+__device__ __forceinline__ uint32_t ldnc(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldnc(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ldnc(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ldnc(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ __half ldnc(const __half* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return __ushort_as_half(v);
+}
+
+// 32 codes of one row from a multiple of 32, as loaded: nothing done with a
+// loaded value here, which would wait for memory at once instead of at the
+// group's next step.  A row ends after whole runs of 16, so the second half may be
+// absent; absent codes decode to 0 (scale and zero 0).
 template <int NBITS>
-struct Codes16 {
-    static constexpr int NW = NBITS == 8 ? 4 : NBITS == 4 ? 2 : NBITS == 3 ? 3 : 1;
+struct Codes32 {
+    static constexpr int NW = NBITS == 3 ? 4 : NBITS;
     uint32_t w[NW];
     uint32_t off;                                // 3 bits: slot of code 0 in w[0]
-    __half2 sz;
+    __half s[2], z[2];                           // of codes 0-15 and 16-31
 };
 
+// halves: 0, 1 or 2 of the runs present; vec: rows and buffer allow whole loads.
 template <int NBITS, bool SMALL>
-__device__ __forceinline__ void load16(const LinearParams& p, int64_t f, bool ok,
-                                       Codes16<NBITS>& c) {
+__device__ __forceinline__ void load32(const LinearParams& p, int64_t f, int halves, bool vec,
+                                       Codes32<NBITS>& c) {
 #pragma unroll
-    for (int i = 0; i < Codes16<NBITS>::NW; ++i) c.w[i] = 0u;
+    for (int i = 0; i < Codes32<NBITS>::NW; ++i) c.w[i] = 0u;
     c.off = 0u;
-    c.sz = __float2half2_rn(0.0f);
-    if (!ok) return;
+    c.s[0] = c.s[1] = c.z[0] = c.z[1] = __float2half_rn(0.0f);
+    if (halves == 0) return;
     if constexpr (NBITS == 3) {
         int64_t w0;
         if (SMALL) w0 = __umulhi(4u * (uint32_t)(f >> 3), 0xCCCCCCCDu) >> 2;    // f / 10
         else w0 = f / 10;
         c.off = (uint32_t)(f - 10 * w0);
         const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed) + w0;
-        c.w[0] = __ldg(src);
-        c.w[1] = __ldg(src + 1);
-        if (c.off > 4u) c.w[2] = __ldg(src + 2);     // only words that hold its codes
+        const uint32_t slots = c.off + 16u * (uint32_t)halves;   // only words that hold them
+        c.w[0] = ldnc(src);
+        c.w[1] = ldnc(src + 1);
+        if (slots > 20u) c.w[2] = ldnc(src + 2);
+        if (slots > 30u) c.w[3] = ldnc(src + 3);
     } else if constexpr (NBITS == 8) {
         const uint2* src = reinterpret_cast<const uint2*>(p.packed + f);
-        const uint2 a = __ldg(src), b = __ldg(src + 1);
-        c.w[0] = a.x; c.w[1] = a.y; c.w[2] = b.x; c.w[3] = b.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < 2 * halves) {
+                const uint2 v = ldnc(src + i);
+                c.w[2 * i] = v.x;
+                c.w[2 * i + 1] = v.y;
+            }
     } else if constexpr (NBITS == 4) {
         const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed) + (f >> 3);
-        c.w[0] = __ldg(src);
-        c.w[1] = __ldg(src + 1);
+        if (vec) {
+            const uint4 v = ldnc(reinterpret_cast<const uint4*>(src));
+            c.w[0] = v.x; c.w[1] = v.y; c.w[2] = v.z; c.w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < 2 * halves) c.w[i] = ldnc(src + i);
+        }
     } else if constexpr (NBITS == 2) {
-        c.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p.packed) + (f >> 4));
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed) + (f >> 4);
+        c.w[0] = ldnc(src);
+        if (halves == 2) c.w[1] = ldnc(src + 1);
     } else {
-        c.w[0] = __ldg(reinterpret_cast<const uint16_t*>(p.packed) + (f >> 4));
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.packed) + (f >> 4);
+        c.w[0] = ldnc(src);
+        if (halves == 2) c.w[0] |= ldnc(src + 1) << 16;
     }
-    c.sz = group_sz(p, f >> p.log2_group);
+    const int64_t g = f >> p.log2_group;
+    c.s[0] = p.sq.codes ? restore_meta_h(p.sq, g) : ldnc(p.scale + g);
+    c.z[0] = p.zq.codes ? restore_meta_h(p.zq, g) : ldnc(p.zero + g);
+    if (p.log2_group == 4 && halves == 2) {
+        c.s[1] = p.sq.codes ? restore_meta_h(p.sq, g + 1) : ldnc(p.scale + g + 1);
+        c.z[1] = p.zq.codes ? restore_meta_h(p.zq, g + 1) : ldnc(p.zero + g + 1);
+    }
 }
 
-// Their fp16 weights: codes 0 .. 7 and 8 .. 15.
+// Their fp16 weights, 8 per unit; one: both halves share the first scale and zero.
 template <int NBITS>
-__device__ __forceinline__ void decode16(const Codes16<NBITS>& c, const Dec3& d, uint4 (&o)[2]) {
-    const float s = __low2float(c.sz), z = __high2float(c.sz);
+__device__ __forceinline__ void decode32(const Codes32<NBITS>& c, bool one, const Dec3& d,
+                                         uint4 (&o)[4]) {
+    const float s0 = __half2float(c.s[0]), z0 = __half2float(c.z[0]);
+    const float s1 = one ? s0 : __half2float(c.s[1]), z1 = one ? z0 : __half2float(c.z[1]);
     if constexpr (NBITS == 3) {
-        // words re-based to codes 0 .. 9 and 10 .. 15 in bits 0 ..
+        // words re-based to codes 10 i .. 10 i + 9 in bits 0 ..; slots 0-3 from the
+        // word, 4-7 from the word >> 12, 8-9 from the word >> 24 (multiply-highs)
         const uint32_t sh = 2u + 3u * c.off;
-        const uint32_t r0 = __funnelshift_r(c.w[0] << 2, c.w[1], sh);
-        const uint32_t r1 = __funnelshift_r(c.w[1] << 2, c.w[2], sh);
-        uint64_t ss, nz;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-        asm("mov.b64 %0, {%1, %1};" : "=l"(nz) : "f"(-z));
-        const uint32_t r0h = __umulhi(r0, d.k20);                 // >> 12
-        o[0].x = pair3_dq<0>(r0, d, nz, ss);
-        o[0].y = pair3_dq<1>(r0, d, nz, ss);
-        o[0].z = pair3_dq<0>(r0h, d, nz, ss);
-        o[0].w = pair3_dq<1>(r0h, d, nz, ss);
-        o[1].x = pair3_dq<0>(__umulhi(r0, d.k8), d, nz, ss);      // >> 24
-        o[1].y = pair3_dq<0>(r1, d, nz, ss);
-        o[1].z = pair3_dq<1>(r1, d, nz, ss);
-        o[1].w = pair3_dq<0>(__umulhi(r1, d.k20), d, nz, ss);
-    } else if constexpr (NBITS == 8) {
-        o[0] = unit8_bytes(c.w[0], c.w[1], z, s);
-        o[1] = unit8_bytes(c.w[2], c.w[3], z, s);
-    } else if constexpr (NBITS == 4) {
-        o[0] = unit8<4>(c.w[0], z, s);
-        o[1] = unit8<4>(c.w[1], z, s);
-    } else if constexpr (NBITS == 2) {
-        o[0] = unit8<2>(c.w[0] & 0xFFFFu, z, s);
-        o[1] = unit8<2>(c.w[0] >> 16, z, s);
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = __funnelshift_r(c.w[i] << 2, i < 3 ? c.w[i < 3 ? i + 1 : 3] : 0u, sh);
+        uint64_t ss[2], nz[2];
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ss[0]) : "f"(s0));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(nz[0]) : "f"(-z0));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ss[1]) : "f"(s1));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(nz[1]) : "f"(-z1));
+        uint32_t v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int sl = (2 * q) % 10, h = q >> 3;
+            const uint32_t x = r[(2 * q) / 10];
+            if (sl == 0) v[q] = pair3_dq<0>(x, d, nz[h], ss[h]);
+            else if (sl == 2) v[q] = pair3_dq<1>(x, d, nz[h], ss[h]);
+            else if (sl == 4) v[q] = pair3_dq<0>(__umulhi(x, d.k20), d, nz[h], ss[h]);
+            else if (sl == 6) v[q] = pair3_dq<1>(__umulhi(x, d.k20), d, nz[h], ss[h]);
+            else v[q] = pair3_dq<0>(__umulhi(x, d.k8), d, nz[h], ss[h]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] = make_uint4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
     } else {
-        o[0] = unit8<1>(c.w[0] & 0xFFu, z, s);
-        o[1] = unit8<1>(c.w[0] >> 8, z, s);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float s = t < 2 ? s0 : s1, z = t < 2 ? z0 : z1;
+            if constexpr (NBITS == 8) o[t] = unit8_bytes(c.w[2 * t], c.w[2 * t + 1], z, s);
+            else if constexpr (NBITS == 4) o[t] = unit8<4>(c.w[t], z, s);
+            else if constexpr (NBITS == 2) o[t] = unit8<2>((c.w[t >> 1] >> (16 * (t & 1))) & 0xFFFFu, z, s);
+            else o[t] = unit8<1>((c.w[0] >> (8 * t)) & 0xFFu, z, s);
+        }
     }
 }
 
@@ -248,15 +312,24 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
     const uint32_t done = bar0 + 8u * (3 * kGmMaxStages);
     volatile int* abrt = &abort_flag;
     auto wait = [&](uint32_t bar, uint32_t ph, bool drain) {
-        if constexpr (CG == 1) mbar_wait(bar, ph, abrt, prm.status, drain);
-        else mbar_wait_cluster(bar, ph, abrt, prm.status, drain);
+        // tries in line (each may be suspended in hardware): the call and its clock
+        // reads cost a step's handshake 0.15 us
+        for (int i = 0; i < kGmTries; ++i)
+            if (mbar_try(bar, ph)) return;
+        mbar_wait(bar, ph, abrt, prm.status, drain);
+    };
+
+    auto wait_cluster = [&](uint32_t bar, uint32_t ph) {
+        for (int i = 0; i < kGmTries; ++i)
+            if (mbar_try_cluster(bar, ph)) return;
+        mbar_wait_cluster(bar, ph, abrt, prm.status, false);
     };
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < S; ++s) {
-            // producer warps of both CTAs, and the peer's staged tokens
-            mbar_init(full_a(s), CG == 1 ? kGmProducers : 2 * kGmProducers + 1);
+            // the producer group's warps, and on the leader the peer's whole stage
+            mbar_init(full_a(s), 4 + (CG == 2 && c2 == 0 ? 1 : 0));
             mbar_init(full_b(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -313,7 +386,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
             uint32_t ph = 0;
             for (int kt = 0; kt < nkt; ++kt) {
                 wait(full_b(s), ph, false);
-                wait(full_a(s), ph, false);
+                if constexpr (CG == 1) wait(full_a(s), ph, false);
+                else wait_cluster(full_a(s), ph);
                 fence_after_sync();
                 const uint32_t a0 = smem_u32(a_st) + (uint32_t)s * kGmABytes;
                 const uint32_t b0 = smem_u32(b_st) + (uint32_t)s * sh.b_bytes;
@@ -328,62 +402,82 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
             gemm_commit<CG>(done, pair);
-        } else if (CG == 2 && lane == 0) {               // the peer's tokens are staged
+        } else if (CG == 2 && lane == 0) {
+            // the peer's stage is whole: one report per stage, by a thread without
+            // memory operations of its own (a producer's arrival at cluster scope would
+            // wait for its code loads in flight)
             int s = 0;
             uint32_t ph = 0;
             for (int kt = 0; kt < nkt; ++kt) {
                 wait(full_b(s), ph, false);
+                wait(full_a(s), ph, false);
                 mbar_arrive_cluster(map_to_rank(full_a(s), leader));
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
     } else {
-        // ---- producers of W_hat: 16 codes a thread and step; the 8 lanes of a
-        // quarter-warp hold 8 rows of one column, so their 16-byte stores hit the
-        // 8 distinct places of the swizzle
+        // ---- producers of W_hat: groups of four warps take the reduction steps in
+        // turn, a thread two runs of 32 codes of its group's steps.  The runs are
+        // decoded before the stage is free, the next step's codes are loaded (they
+        // have the other groups' steps to arrive), then the weights are stored.  The
+        // 8 lanes of a quarter-warp hold 8 rows of one column, so their 16-byte
+        // stores hit the 8 distinct places of the swizzle.
         Dec3 dec;
         if constexpr (NBITS == 3) dec.init();
-        const int pw = warp - 2;
-        const int r = TRANS ? (pw & 7) * 8 + (lane & 7) : pw * 8 + (lane & 7);
-        const int j = TRANS ? (pw >> 3) * 4 + (lane >> 3) : lane >> 3;     // 16 codes from 16 j
-        const int64_t row0 = TRANS ? (int64_t)kt0 * kGmK + r : n0 + r;
-        const int64_t col0 = TRANS ? n0 + 16 * j : (int64_t)kt0 * kGmK + 16 * j;
-        auto fetch = [&](int kt, Codes16<NBITS>& c) {
-            const int64_t row = TRANS ? row0 + (int64_t)kt * kGmK : row0;
-            const int64_t col = TRANS ? col0 : col0 + (int64_t)kt * kGmK;
-            load16<NBITS, SMALL>(prm, row * prm.K + col, row < prm.N && col < prm.K, c);
+        const int group = (warp - 2) >> 2, w4 = (warp - 2) & 3;
+        // run q: layer: row r + 64 q, codes 32 j .. (j < 2); TRANS: row r + 8 q,
+        // codes 32 j .. (j < 4)
+        const int r = 16 * w4 + (lane & 7) + (TRANS ? 0 : 8 * (lane >> 4));
+        const int j = TRANS ? lane >> 3 : (lane >> 3) & 1;
+        constexpr int kRunRows = TRANS ? 8 : 64;
+        const int64_t row0 = (TRANS ? (int64_t)kt0 * kGmK : n0) + r;
+        const int64_t col0 = (TRANS ? n0 : (int64_t)kt0 * kGmK) + 32 * j;
+        const int64_t f0 = row0 * prm.K + col0;
+        const bool one = prm.log2_group > 4, vec = sh.vec != 0;
+        Codes32<NBITS> raw[2];
+        auto fetch = [&](int kt) {
+            const int64_t at = (int64_t)kt * kGmK, f = f0 + (TRANS ? at * prm.K : at);
+            const int64_t left = prm.K - col0 - (TRANS ? 0 : at);
+            const int halves = left >= 32 ? 2 : left > 0 ? 1 : 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                load32<NBITS, SMALL>(prm, f + (int64_t)(q * kRunRows) * prm.K,
+                                     row0 + q * kRunRows + (TRANS ? at : 0) < prm.N ? halves : 0,
+                                     vec, raw[q]);
         };
-        // places of the thread's two 16-byte units in the tile
-        const uint32_t base = (uint32_t)r * 128u + (TRANS ? (uint32_t)(j >> 2) * kGmHalf : 0u);
-        const uint32_t u0 = base + ((uint32_t)(((2 * j) & 7) ^ (r & 7)) << 4);
-        const uint32_t u1 = base + ((uint32_t)(((2 * j + 1) & 7) ^ (r & 7)) << 4);
-        Codes16<NBITS> ring[kGmAhead];
+        // places of a run's 16-byte units in the tile
+        uint32_t place[4];
 #pragma unroll
-        for (int u = 0; u < kGmAhead - 1; ++u)
-            if (u < nkt) fetch(u, ring[u]);
-        int s = 0;
-        uint32_t ph = 1;
-        for (int kb = 0; kb < nkt; kb += kGmAhead) {
+        for (int t = 0; t < 4; ++t)
+            place[t] = (uint32_t)r * 128u + (TRANS ? (uint32_t)(j >> 1) * kGmHalf : 0u) +
+                       ((uint32_t)((4 * (j & 1) + t) ^ (r & 7)) << 4);
+        if (group < nkt) fetch(group);
+        int s = group % S;
+        uint32_t ph = 1u ^ ((uint32_t)(group / S) & 1u);
+        for (int kt = group; kt < nkt; kt += kGmGroups) {
+            uint4 o[2][4];
 #pragma unroll
-            for (int u = 0; u < kGmAhead; ++u) {
-                const int kt = kb + u;
-                if (kt < nkt) {
-                    if (kt + kGmAhead - 1 < nkt)
-                        fetch(kt + kGmAhead - 1, ring[(u + kGmAhead - 1) % kGmAhead]);
-                    uint4 o[2];
-                    decode16<NBITS>(ring[u], dec, o);
-                    wait(empty(s), ph, false);
-                    uint8_t* tile = a_st + (uint32_t)s * kGmABytes;
-                    *reinterpret_cast<uint4*>(tile + u0) = o[0];
-                    *reinterpret_cast<uint4*>(tile + u1) = o[1];
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 1) mbar_arrive(full_a(s));
-                        else mbar_arrive_cluster(map_to_rank(full_a(s), leader));
-                    }
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                }
+            for (int q = 0; q < 2; ++q) {
+                // a lone first half: its scale must not decode the absent second one
+                const bool whole = TRANS ? prm.K - col0 >= 32
+                                         : prm.K - col0 - (int64_t)kt * kGmK >= 32;
+                decode32<NBITS>(raw[q], one && whole, dec, o[q]);
+            }
+            if (kt + kGmGroups < nkt) fetch(kt + kGmGroups);
+            wait(empty(s), ph, false);
+            uint8_t* tile = a_st + (uint32_t)s * kGmABytes;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<uint4*>(tile + place[t] + (uint32_t)(q * kRunRows * 128)) = o[q][t];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_a(s));
+            s += kGmGroups;
+            while (s >= S) {
+                s -= S;
+                ph ^= 1u;
             }
         }
     }
@@ -517,6 +611,7 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     sh.bn = plan.bn;
     sh.nmma = plan.bn > 256 ? plan.bn / 2 : plan.bn;
     sh.ks = plan.ks;
+    sh.vec = prm.K % 32 == 0 && (reinterpret_cast<uintptr_t>(prm.packed) & 15u) == 0;
     sh.b_bytes = (uint32_t)(plan.bn / CG) * 128u;
     const uint32_t fit = kGmStageBytes / (kGmABytes + sh.b_bytes);
     sh.stages = (int)(fit < (uint32_t)kGmMaxStages ? fit : (uint32_t)kGmMaxStages);
