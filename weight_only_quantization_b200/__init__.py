@@ -427,27 +427,41 @@ def hqq_lowrank(W, q: QuantizedMatrix, rank: int, omega, power_iters: int = 2, w
     return B, A, sigma
 
 
+_DTYPES = {}
+
+
 def _dtype_code(dtype, name):
     """hqq_dtype of a torch dtype."""
-    import torch
-    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be float16, bfloat16 or float32")
     return code
 
 
-def _on_device_of(t, stream, *others):
-    """Check that the given tensors live on t's device, and return (context
-    that makes it the current device, stream handle there)."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run_on(t, stream, others, fn, *args):
+    """fn(*args, stream) with t's device current; every other tensor given must
+    live there, and so must the stream (None: the device's current one)."""
     import torch
+    dev = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != dev:
             raise ValueError(f"all tensors must be on {t.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
+        stream = torch.cuda.current_stream(dev)
     elif stream.device != t.device:
         raise ValueError(f"stream must be on {t.device}")
-    return torch.cuda.device(t.device), ctypes.c_void_p(stream.cuda_stream)
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream))
 
 
 def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher_lse=None,
@@ -484,23 +498,22 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
     elif grad.dtype != logits.dtype or grad.shape != logits.shape or \
             (vocab > 1 and grad.stride(1) != 1):
         raise ValueError("grad must be like logits")
-    ctx, st = _on_device_of(logits, stream, top_logits, top_index, teacher_lse, weight, grad,
-                            loss, lse)
     if loss is None:
         loss = torch.empty(tokens, dtype=torch.float32, device=logits.device)
     if lse is None:
         lse = torch.empty(tokens, dtype=torch.float32, device=logits.device)
     # (a single row may report any stride)
-    rows = max(logits.stride(0), vocab) if tokens > 1 else vocab
-    grows = 0 if grad is None else max(grad.stride(0), vocab) if tokens > 1 else vocab
-    if tokens > 1 and (logits.stride(0) < vocab or (grad is not None and grad.stride(0) < vocab)):
-        raise ValueError("rows of logits and grad must not overlap")
-    with ctx:
-        _check(_lib.hqq_distill(_ptr(logits), rows, dt, tokens, vocab, _ptr(top_logits),
-                                _dtype_code(top_logits.dtype, "top_logits"), _ptr(top_index),
-                                top_index.element_size(), top_logits.shape[1],
-                                float(temperature), _ptr(teacher_lse), _ptr(weight), _ptr(loss),
-                                _ptr(lse), _ptr(grad), grows, st))
+    rows = grows = vocab
+    if tokens > 1:
+        rows = logits.stride(0)
+        grows = vocab if grad is None else grad.stride(0)
+        if rows < vocab or grows < vocab:
+            raise ValueError("rows of logits and grad must not overlap")
+    _run_on(logits, stream, (top_logits, top_index, teacher_lse, weight, grad, loss, lse),
+            _lib.hqq_distill, logits.data_ptr(), rows, dt, tokens, vocab, top_logits.data_ptr(),
+            _dtype_code(top_logits.dtype, "top_logits"), top_index.data_ptr(),
+            top_index.element_size(), top_logits.shape[1], temperature, _addr(teacher_lse),
+            _addr(weight), loss.data_ptr(), lse.data_ptr(), _addr(grad), grows)
     return loss, lse, grad
 
 
@@ -513,64 +526,71 @@ class Adapters:
     scaling: "torch.Tensor | None" = None   # fp32 [count]; None: 1
 
     def _c(self, rows: int, cols: int):
-        A, B = self.A, self.B
+        A, B, scaling = self.A, self.B, self.scaling
         if A.dim() == 2:
             A = A.unsqueeze(0)
         if B.dim() == 2:
             B = B.unsqueeze(0)
-        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or \
-                A.shape[1] != B.shape[2] or A.shape[2] != cols or B.shape[1] != rows:
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("adapters must be A [count, rank, cols] and B [count, rows, rank]")
+        count, rank, ac = A.shape
+        if B.shape != (count, rows, rank) or ac != cols:
             raise ValueError("adapters must be A [count, rank, cols] and B [count, rows, rank]")
         if A.dtype != B.dtype:
             raise ValueError("A and B must have the same type")
-        count, rank = A.shape[0], A.shape[1]
-        for t, nm in ((A, "A"), (B, "B")):
-            if not t.is_cuda or (t.numel() and not t[0].is_contiguous()):
-                raise ValueError(f"each adapter's {nm} must be a contiguous CUDA matrix")
-            if count > 1 and t.stride(0) < t.shape[1] * t.shape[2]:
-                raise ValueError(f"the adapters of {nm} must not overlap")
-        if self.scaling is not None:
-            _check_tensor(self.scaling, "scaling")
-            import torch
-            if self.scaling.dtype != torch.float32 or self.scaling.numel() != count:
+        a_stride = b_stride = 0
+        if not (A.is_contiguous() and B.is_contiguous()):
+            for t, nm in ((A, "A"), (B, "B")):
+                if t.numel() and not t[0].is_contiguous():
+                    raise ValueError(f"each adapter's {nm} must be a contiguous matrix")
+                if count > 1 and t.stride(0) < t.shape[1] * t.shape[2]:
+                    raise ValueError(f"the adapters of {nm} must not overlap")
+            if count > 1:
+                a_stride, b_stride = A.stride(0), B.stride(0)
+        if not (A.is_cuda and B.is_cuda):
+            raise ValueError("adapters must be CUDA tensors")
+        s = None
+        if scaling is not None:
+            _check_tensor(scaling, "scaling")
+            if _dtype_code(scaling.dtype, "scaling") != 2 or scaling.numel() != count:
                 raise ValueError("scaling must be a float32 [count] tensor")
-        return _CAdapters(A.data_ptr(), B.data_ptr(),
-                          None if self.scaling is None else self.scaling.data_ptr(),
-                          A.stride(0) if count > 1 else 0, B.stride(0) if count > 1 else 0,
-                          count, rank, _dtype_code(A.dtype, "adapters"))
+            s = scaling.data_ptr()
+        return _CAdapters(A.data_ptr(), B.data_ptr(), s, a_stride, b_stride, count, rank,
+                          _dtype_code(A.dtype, "adapters"))
 
 
-def _adapter_call(x, q, adapters, index, zero_q, scale_q, M, backward, workspace, extra, stream):
-    """What both adapter calls check and marshal."""
+def _adapter_call(fn, lead, tail, x, q, adapters, index, zero_q, scale_q, M, backward, workspace,
+                  tensors, stream):
+    """What both adapter calls check and marshal: fn(*lead, matrix, adapters, index, *tail,
+    workspace, its bytes, stream)."""
     import torch
     if index is not None and (index.dtype != torch.int32 or index.numel() != M):
         raise ValueError("index must be an int32 [M] tensor")
-    for t, nm in ((q.packed, "packed"), (index, "index"), (workspace, "workspace"), *extra):
-        _check_tensor(t, nm)
     zero = q.zero if zero_q is None else None
     scale = q.scale if scale_q is None else None
-    for t, nm in ((zero, "zero"), (scale, "scale")):
+    for t, nm in ((q.packed, "packed"), (index, "index"), (workspace, "workspace"),
+                  (zero, "zero"), (scale, "scale"), *tensors):
         _check_tensor(t, nm)
-    ca = None if adapters is None else adapters._c(q.rows, q.cols)
-    more = [] if adapters is None else [adapters.A, adapters.B, adapters.scaling]
+    used = [q.packed, index, workspace, zero, scale, *(t for t, _ in tensors)]
+    ca, rank, count = None, 0, 0
+    if adapters is not None:
+        ca = adapters._c(q.rows, q.cols)
+        rank, count = ca.rank, ca.count
+        used += (adapters.A, adapters.B, adapters.scaling)
     for m in (zero_q, scale_q):
         if m is not None:
-            more += [m.codes, m.scale, m.zero]
-    ctx, st = _on_device_of(x, stream, q.packed, zero, scale, index, workspace,
-                            *more, *(t for t, _ in extra))
-    need = _lib.hqq_linear_adapters_workspace_bytes(M, q.rows, q.cols,
-                                                    0 if ca is None else ca.rank,
-                                                    0 if ca is None else ca.count, backward)
+            used += (m.codes, m.scale, m.zero)
+    need = _lib.hqq_linear_adapters_workspace_bytes(M, q.rows, q.cols, rank, count, backward)
     if need < 0:
-        raise HQQError(2 if ca is None or (0 < ca.rank <= 512 and 0 < ca.count <= 65535) else 4)
+        raise HQQError(2 if ca is None or (0 < rank <= 512 and 0 < count <= 65535) else 4)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    matrix = (_ptr(q.packed), _ptr(scale), _ptr(zero),
-              None if zero_q is None else ctypes.byref(zero_q._c()),
-              None if scale_q is None else ctypes.byref(scale_q._c()),
-              q.rows, q.cols, q.nbits, q.group, None if ca is None else ctypes.byref(ca))
-    return ctx, st, matrix, workspace, 0 if workspace is None else workspace.numel() * \
-        workspace.element_size()
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    byref = ctypes.byref
+    _run_on(x, stream, used, fn, *lead, M, q.packed.data_ptr(), _addr(scale), _addr(zero),
+            None if zero_q is None else byref(zero_q._c()),
+            None if scale_q is None else byref(scale_q._c()), q.rows, q.cols, q.nbits, q.group,
+            None if ca is None else byref(ca), _addr(index), *tail, _addr(workspace), nbytes)
 
 
 def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, out=None,
@@ -588,12 +608,9 @@ def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, o
         out = torch.empty((M, q.rows), dtype=torch.float16, device=X.device)
     elif out.dtype != torch.float16 or out.numel() != M * q.rows:
         raise ValueError("out must be a float16 [M, rows] tensor")
-    ctx, st, matrix, workspace, nbytes = _adapter_call(
-        X, q, adapters, index, zero_q, scale_q, M, 0, workspace,
-        ((X, "X"), (out, "out"), (status, "status")), stream)
-    with ctx:
-        _check(_lib.hqq_linear_adapters(_ptr(X), M, *matrix, _ptr(index), _ptr(out), _ptr(status),
-                                        _ptr(workspace), nbytes, st))
+    _adapter_call(_lib.hqq_linear_adapters, (X.data_ptr(),), (out.data_ptr(), _addr(status)), X, q,
+                  adapters, index, zero_q, scale_q, M, 0, workspace,
+                  ((X, "X"), (out, "out"), (status, "status")), stream)
     return out
 
 
@@ -636,11 +653,9 @@ def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters |
                              "[count, rows, rank] tensors")
     else:
         dA = dB = None
-    ctx, st, matrix, workspace, nbytes = _adapter_call(
-        dY, q, adapters, index, zero_q, scale_q, M, 1, workspace,
-        ((dY, "dY"), (X, "X"), (dX, "dX"), (dA, "dA"), (dB, "dB"), (status, "status")), stream)
-    with ctx:
-        _check(_lib.hqq_linear_adapters_backward(_ptr(dY), _ptr(X), M, *matrix, _ptr(index),
-                                                 _ptr(dX), _ptr(dA), _ptr(dB), _ptr(status),
-                                                 _ptr(workspace), nbytes, st))
+    _adapter_call(_lib.hqq_linear_adapters_backward, (dY.data_ptr(), _addr(X)),
+                  (_addr(dX), _addr(dA), _addr(dB), _addr(status)), dY, q, adapters, index, zero_q,
+                  scale_q, M, 1, workspace,
+                  ((dY, "dY"), (X, "X"), (dX, "dX"), (dA, "dA"), (dB, "dB"), (status, "status")),
+                  stream)
     return dX, dA, dB

@@ -567,17 +567,26 @@ struct GemmPlan {
     int cg, ks, bn;
 };
 
-// Tile choice.  A reduction step of a CTA takes about max(kStep, kToken bn) us
-// (decoding 128 x 64 weights, or the MMAs of bn tokens), a tile kTile us besides
-// its steps and a split kSplit more; the tiles run in rounds of one CTA per SM.
+// Tile choice, from the times of every (CG, ks, bn) on four matrices and 64 to
+// 2048 tokens: a round of tiles takes its reduction steps plus a fixed part,
+//   CG = 1   0.60 us a step whatever bn (producers and handshakes),
+//   CG = 2   max(0.74, 0.0019 bn) us a step (the handshake between the CTAs; from
+//            384 tokens the MMAs),
+// e.g. 4096 x 4096 at 4 bits (64 steps): 256 tokens 47 us as one CTA, 32 split by 2
+// and 23 split by 4; 2048 tokens 96 us in tiles of 256 and 73 in pairs of 512.  A
+// round holds one CTA per SM, fewer where clusters leave part of a GPC's SMs
+// over: four-CTA clusters reach 16 SMs of 18, and of eight CTAs only a few run at
+// once (splits by 8 measured slower wherever more than 8 clusters were needed).
 GemmPlan plan_gemm(int64_t M, int64_t features, int64_t depth, int sms) {
-    constexpr double kStep = 0.50, kToken = 0.00155, kTile = 5.0, kSplit = 3.0;
     const int64_t steps = (depth + kGmK - 1) / kGmK, tiles = (features + kGmM - 1) / kGmM;
     GemmPlan best = {1, 1, 16};
     double cost = 1e30;
     for (int cg = 1; cg <= 2; ++cg)
         for (int ks = 1; ks * cg <= 8; ks *= 2) {
             if (ks > 1 && steps < 4 * ks) break;
+            const int size = cg * ks;
+            const int64_t slots = size == 1 ? sms : size == 2 ? sms / 2 * 2
+                                  : size == 4 ? sms * 16 / 18 / 4 * 4 : 64;
             // bn: every MMA a multiple of 16 tokens a CTA (above 256 two MMAs), every
             // share of a split a multiple of 8
             const int unit = 8 * ks > 16 * cg ? 8 * ks : 16 * cg, most = 256 * cg;
@@ -585,12 +594,12 @@ GemmPlan plan_gemm(int64_t M, int64_t features, int64_t depth, int sms) {
             int bn = whole < most ? (int)whole : most;
             if (bn > 256) bn = (bn + 63) / 64 * 64;
             for (; bn > 0; bn -= bn > 256 ? 64 : unit > 32 ? unit : 32) {
-                const int64_t ctas = (M + bn - 1) / bn * ((tiles + cg - 1) / cg) * cg * ks;
-                const int64_t slots = sms / cg * cg;
+                const int64_t ctas = (M + bn - 1) / bn * ((tiles + cg - 1) / cg) * size;
+                if (size == 8 && ctas > slots) break;
                 const double rounds = (double)((ctas + slots - 1) / slots);
-                const double step = kStep > kToken * bn ? kStep : kToken * bn;
-                const double c = rounds * ((double)((steps + ks - 1) / ks) * step + kTile +
-                                           (ks > 1 ? kSplit : 0.0) + 0.004 * bn / ks);
+                const double step = cg == 1 ? 0.60 : 0.0019 * bn > 0.74 ? 0.0019 * bn : 0.74;
+                const double c = rounds * ((double)((steps + ks - 1) / ks) * step +
+                                           (cg == 1 ? 8.5 : 13.0) + (ks > 1 ? 0.02 : 0.01) * bn);
                 if (c < cost) {
                     cost = c;
                     best = {cg, ks, bn};
