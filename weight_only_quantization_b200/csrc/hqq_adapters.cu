@@ -86,6 +86,10 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 enum FactorForm {
     kKPairs,     // fp16, the reduction index contiguous: one 16-byte load a lane
     kJPairs,     // fp16, the rank contiguous: 8x8 blocks transposed in registers
+    kKBf16,      // tf32 MMAs: bf16 or fp32, the reduction index contiguous (16-byte
+    kKF32,       //   loads) ..
+    kJBf16,      //   .. or the rank contiguous (a sector of 8 or 16 ranks a row)
+    kJF32,
     kAnyType     // any type and strides, tf32 MMAs
 };
 
@@ -113,6 +117,10 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
     const int slot = (int)(cl % (unsigned)slots);
     const int64_t m0 = (int64_t)(cl / (unsigned)slots) * kShTokens;
     const int j0 = (int)blockIdx.y * RC;
+
+    // the kernel that reads T may start its own work (it waits for this one's end
+    // before it reads)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // the lane's token and its adapter (-1: none)
     int mine = -1;
@@ -147,7 +155,7 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[b][n][e] = 0.0f;
 
-#pragma unroll 2
+#pragma unroll 1
         for (int64_t bl = (int64_t)crank * kShWarps + warp; bl < blocks; bl += bstep) {
             const int64_t k0 = bl * 32, kk = k0 + 8 * t;
             uint4 x[2][2];
@@ -208,28 +216,89 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
                         }
                 }
             } else {
+                constexpr bool k32 = FORM == kKF32 || FORM == kJF32;
+                // the lane's values for each n-tile: rank j0 + 8 n + g, k = kk .. kk + 7
+                float v[NT][8];
+                if constexpr (FORM == kKBf16 || FORM == kKF32) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int j = j0 + 8 * n + g;
-                    float v[8];
+                    for (int n = 0; n < NT; ++n) {
+                        const int j = j0 + 8 * n + g;
+                        const bool in = j < p.rank && kk < p.K;
+                        if constexpr (FORM == kKBf16) {
+                            const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(
+                                                     static_cast<const __nv_bfloat16*>(p.F) + fo + j * p.sj + kk))
+                                               : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = j < p.rank && kk + i < p.K
-                                   ? factor_val(p.F, p.dtype, fo + j * p.sj + (kk + i) * p.sk)
-                                   : 0.0f;
+                            for (int i = 0; i < 4; ++i) {
+                                v[n][2 * i] = __uint_as_float(word_of(u, i) << 16);
+                                v[n][2 * i + 1] = __uint_as_float(word_of(u, i) & 0xffff0000u);
+                            }
+                        } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h0, l0, h1, l1;
-                        split_tf32(v[2 * i], h0, l0);
-                        split_tf32(v[2 * i + 1], h1, l1);
+                            for (int h = 0; h < 2; ++h) {
+                                const float4 u = in ? __ldg(reinterpret_cast<const float4*>(
+                                                          static_cast<const float*>(p.F) + fo + j * p.sj + kk) + h)
+                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                v[n][4 * h] = u.x;
+                                v[n][4 * h + 1] = u.y;
+                                v[n][4 * h + 2] = u.z;
+                                v[n][4 * h + 3] = u.w;
+                            }
+                        }
+                    }
+                } else if constexpr (FORM == kJBf16 || FORM == kJF32) {
+                    const int64_t base = fo + kk * p.sk + j0 + g;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t at = base + i * p.sk;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const bool in = j0 + 8 * n + g < p.rank && kk + i < p.K;
+                            if constexpr (FORM == kJF32)
+                                v[n][i] = in ? __ldg(static_cast<const float*>(p.F) + at + 8 * n) : 0.0f;
+                            else
+                                v[n][i] = in ? __bfloat162float(__ldg(
+                                                   static_cast<const __nv_bfloat16*>(p.F) + at + 8 * n))
+                                             : 0.0f;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int j = j0 + 8 * n + g;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[n][i] = j < p.rank && kk + i < p.K
+                                          ? factor_val(p.F, p.dtype, fo + j * p.sj + (kk + i) * p.sk)
+                                          : 0.0f;
+                    }
+                }
+                const bool split = k32 || (FORM == kAnyType && p.dtype == 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t xa[2][4];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t w0 = word_of(x[b][0], i), w1 = word_of(x[b][1], i);
+                        xa[b][0] = half_bits_f32(w0, 0);
+                        xa[b][1] = half_bits_f32(w1, 0);
+                        xa[b][2] = half_bits_f32(w0, 1);
+                        xa[b][3] = half_bits_f32(w1, 1);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t h0 = __float_as_uint(v[n][2 * i]), h1 = __float_as_uint(v[n][2 * i + 1]);
+                        uint32_t l0 = 0u, l1 = 0u;
+                        if (split) {
+                            split_tf32(v[n][2 * i], h0, l0);
+                            split_tf32(v[n][2 * i + 1], h1, l1);
+                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
                             if (has[b]) {
-                                const uint32_t w0 = word_of(x[b][0], i), w1 = word_of(x[b][1], i);
-                                const uint32_t a0 = half_bits_f32(w0, 0), a1 = half_bits_f32(w1, 0);
-                                const uint32_t a2 = half_bits_f32(w0, 1), a3 = half_bits_f32(w1, 1);
-                                if (p.dtype == 2) mma_tf32(acc[b][n], a0, a1, a2, a3, l0, l1);
-                                mma_tf32(acc[b][n], a0, a1, a2, a3, h0, h1);
+                                if (split)
+                                    mma_tf32(acc[b][n], xa[b][0], xa[b][1], xa[b][2], xa[b][3], l0, l1);
+                                mma_tf32(acc[b][n], xa[b][0], xa[b][1], xa[b][2], xa[b][3], h0, h1);
                             }
                     }
                 }
@@ -305,8 +374,10 @@ cudaError_t launch_shrink_nt(const ShrinkParams& p, cudaStream_t stream) {
     int64_t slots = p.count < kShTokens ? p.count : kShTokens;
     if (p.M < slots) slots = p.M;
     while (slots > 1 && tiles * slots > 256) slots = (slots + 1) / 2;
+    // split the reduction while the grid stays within two CTAs per SM and every warp
+    // keeps two steps
     int csize = 1;
-    while (csize < kShMaxCluster && tiles * chunks * csize < 4 * sms &&
+    while (csize < kShMaxCluster && tiles * chunks * csize <= sms &&
            blocks >= (int64_t)2 * csize * kShWarps)
         csize *= 2;
     auto kern = shrink_kernel<FORM, NT>;
@@ -375,7 +446,7 @@ order_kernel(const int32_t* __restrict__ index, int64_t M, int count, int32_t* _
 constexpr int kFgThreads = 256;
 constexpr int kFgCols = 64;              // columns of X or dY per CTA
 constexpr int kFgTokens = 64;            // tokens per stage
-constexpr int kFgStages = 3;
+constexpr int kFgStages = 2;
 constexpr int kFgMaxCluster = 4;
 constexpr int kFgZ = kFgCols + 16;       // halves per staged row: 8 rows apart in the banks
 
@@ -384,7 +455,7 @@ struct FgGeo {
     static constexpr int RC = 8 * NT;
     static constexpr int SS = RC + 8;    // floats per staged row of T or P
     static constexpr int STAGE = kFgTokens * (kFgZ * 2 + SS * 4);
-    static constexpr int RED = 2 * kFgCols * RC * 4;             // both token halves
+    static constexpr int RED = 4 * kFgCols * RC * 4;             // the token quarters
     static constexpr int XRED = (kFgMaxCluster - 1) * kFgCols * RC * 4;
     static constexpr int BYTES = kFgStages * STAGE > RED + XRED ? kFgStages * STAGE : RED + XRED;
 };
@@ -406,6 +477,8 @@ factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
     const int g = lane >> 2, t = lane & 3;
     const int crank = csize == 1 ? 0 : (int)(blockIdx.x % (unsigned)csize);
     const int tile = (int)(csize == 1 ? blockIdx.x : blockIdx.x / (unsigned)csize);
+    // (the input gradient's kernel may start its own work)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int a = (int)blockIdx.y, j0 = (int)blockIdx.z * RC;
     const bool isA = tile < p.tiles_a;
     const __half* Z = isA ? p.X : p.dY;
@@ -442,82 +515,105 @@ factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    float sum[NT][4];
+    float sum[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[n][e] = 0.0f;
-    const int cg16 = (warp & 3) * 16, th = (warp >> 2) * 32;      // columns, tokens of the warp
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[b][n][e] = 0.0f;
+    const int cols32 = (warp & 1) * 32, th = (warp >> 1) * 16;    // columns, tokens of the warp
 
 #pragma unroll
     for (int s = 0; s < kFgStages - 1; ++s) fill(crank + (int64_t)s * csize, s);
     int it = 0;
     for (int64_t c = crank; c < chunks; c += csize, ++it) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kFgStages - 2) : "memory");
-        __syncthreads();
         fill(c + (int64_t)(kFgStages - 1) * csize, (it + kFgStages - 1) % kFgStages);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kFgStages - 1) : "memory");
+        __syncthreads();
         const uint8_t* st = fg_smem + (it % kFgStages) * G::STAGE;
         const __half* zs = reinterpret_cast<const __half*>(st);
         const float* ss = reinterpret_cast<const float*>(st + kFgTokens * kFgZ * 2);
-        float acc[NT][4];
+        float acc[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k8 = 0; k8 < 4; ++k8) {
+                for (int e = 0; e < 4; ++e) acc[b][n][e] = 0.0f;
+#pragma unroll
+        for (int k8 = 0; k8 < 2; ++k8) {
             const int r0 = th + 8 * k8 + t, r1 = r0 + 4;
-            // MMA rows g and g + 8 are columns 2g and 2g + 1 of the warp's 16
-            const uint32_t z0 = *reinterpret_cast<const uint32_t*>(zs + r0 * kFgZ + cg16 + 2 * g);
-            const uint32_t z1 = *reinterpret_cast<const uint32_t*>(zs + r1 * kFgZ + cg16 + 2 * g);
-            const uint32_t a0 = half_bits_f32(z0, 0), a1 = half_bits_f32(z0, 1);
-            const uint32_t a2 = half_bits_f32(z1, 0), a3 = half_bits_f32(z1, 1);
+            // MMA rows g and g + 8 of block b are columns 2g and 2g + 1 of its 16
+            uint32_t a[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int c = cols32 + 16 * b + 2 * g;
+                const uint32_t z0 = *reinterpret_cast<const uint32_t*>(zs + r0 * kFgZ + c);
+                const uint32_t z1 = *reinterpret_cast<const uint32_t*>(zs + r1 * kFgZ + c);
+                a[b][0] = half_bits_f32(z0, 0);
+                a[b][1] = half_bits_f32(z0, 1);
+                a[b][2] = half_bits_f32(z1, 0);
+                a[b][3] = half_bits_f32(z1, 1);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint32_t h0, l0, h1, l1;
                 split_tf32(ss[r0 * G::SS + 8 * n + g], h0, l0);
                 split_tf32(ss[r1 * G::SS + 8 * n + g], h1, l1);
-                mma_tf32(acc[n], a0, a1, a2, a3, l0, l1);
-                mma_tf32(acc[n], a0, a1, a2, a3, h0, h1);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    mma_tf32(acc[b][n], a[b][0], a[b][1], a[b][2], a[b][3], l0, l1);
+                    mma_tf32(acc[b][n], a[b][0], a[b][1], a[b][2], a[b][3], h0, h1);
+                }
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[n][e] = __fadd_rn(sum[n][e], acc[n][e]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[b][n][e] = __fadd_rn(sum[b][n][e], acc[b][n][e]);
+        // (with two stages the next fill overwrites the one just read)
+        __syncthreads();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();                                     // the stages are free
 
-    // both token halves, then the cluster's parts, as [column][rank]
+    // the token quarters, then the cluster's parts, as [column][rank]
+    constexpr int RE = kFgCols * RC;
     float* red = reinterpret_cast<float*>(fg_smem);
-    float* xred = red + 2 * kFgCols * RC;
+    float* xred = red + 4 * RE;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            red[((warp >> 2) * kFgCols + cg16 + 2 * g + (e >> 1)) * RC + 8 * n + 2 * t + (e & 1)] =
-                sum[n][e];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[(warp >> 1) * RE + (cols32 + 16 * b + 2 * g + (e >> 1)) * RC + 8 * n + 2 * t + (e & 1)] =
+                    sum[b][n][e];
     __syncthreads();
+    auto quarters = [&](int e) {
+        return __fadd_rn(__fadd_rn(red[e], red[RE + e]), __fadd_rn(red[2 * RE + e], red[3 * RE + e]));
+    };
     if (csize > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (crank != 0) {
-            float* dst = cg::this_cluster().map_shared_rank(xred, 0) + (crank - 1) * kFgCols * RC;
-            for (int e = tid; e < kFgCols * RC; e += kFgThreads)
-                dst[e] = __fadd_rn(red[e], red[kFgCols * RC + e]);
+            float* dst = cg::this_cluster().map_shared_rank(xred, 0) + (crank - 1) * RE;
+            for (int e = tid; e < RE; e += kFgThreads) dst[e] = quarters(e);
         }
         asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     if (crank != 0) return;
-    for (int i = tid; i < kFgCols * RC; i += kFgThreads) {
+    for (int i = tid; i < RE; i += kFgThreads) {
         // dA is stored [rank][column], dB [column][rank]: adjacent threads write
         // adjacent values of either
         const int col = isA ? i % kFgCols : i / RC, j = isA ? i / kFgCols : i % RC;
         const int e = col * RC + j;
-        float v = __fadd_rn(red[e], red[kFgCols * RC + e]);
-        for (int c = 1; c < csize; ++c) v = __fadd_rn(v, xred[(c - 1) * kFgCols * RC + e]);
+        float v = quarters(e);
+        for (int c = 1; c < csize; ++c) v = __fadd_rn(v, xred[(c - 1) * RE + e]);
         if (c0 + col < cols && j0 + j < p.rank) {
             if (isA) p.dA[((int64_t)a * p.rank + j0 + j) * p.K + c0 + col] = v;
             else p.dB[((int64_t)a * p.N + c0 + col) * p.rank + j0 + j] = v;
@@ -576,6 +672,13 @@ cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
     if (p.dtype == 0 && p.sj == 1 && (addr & 3u) == 0 && p.rank % 2 == 0 && p.sk % 2 == 0 &&
         p.sa % 2 == 0)
         return launch_shrink_form<kJPairs>(p, stream);
+    if (p.dtype != 0 && p.sk == 1 && (addr & 15u) == 0 && p.sj % 8 == 0 && p.sa % 8 == 0 &&
+        p.K % 8 == 0)
+        return p.dtype == 1 ? launch_shrink_form<kKBf16>(p, stream)
+                            : launch_shrink_form<kKF32>(p, stream);
+    if (p.dtype != 0 && p.sj == 1)
+        return p.dtype == 1 ? launch_shrink_form<kJBf16>(p, stream)
+                            : launch_shrink_form<kJF32>(p, stream);
     return launch_shrink_form<kAnyType>(p, stream);
 }
 

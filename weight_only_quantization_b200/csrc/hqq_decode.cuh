@@ -552,6 +552,7 @@ decode_kernel(const __half* __restrict__ X, const __grid_constant__ LinearParams
                 if (u * kDcThreads + t < TW)
                     for (int c = 1; c < split; ++c) v[u] += cred[(c - 1) * TW + u * kDcThreads + t];
     }
+    if constexpr (AD) wait_for_T();
     if (rank == 0) {
 #pragma unroll
         for (int u = 0; u * kDcThreads < TW; ++u) {
@@ -733,6 +734,7 @@ decode_sx_kernel(const __half* __restrict__ X, const __grid_constant__ LinearPar
                     for (int e = 0; e < 4; ++e)
                         acc[c][e] += cred[((q - 1) * kDcWarps + warp) * TW + (4 * c + e) * 32 + lane];
     }
+    if constexpr (AD) wait_for_T();
     if (rank == 0) {
 #pragma unroll
         for (int c = 0; c < NT; ++c)
@@ -765,22 +767,24 @@ cudaError_t launch_sx(const LinearParams& p, const LowRankEpi& lr, const void* X
     int split = 1;
     while (split < kDcMaxSplit && ctiles * split < 2 * sms && nchunk >= 4 * split) split *= 2;
     const __half* xp = static_cast<const __half*>(X);
-    if (split == 1) {
+    if (split == 1 && !AD) {
         kern<<<(unsigned)ctiles, kDcThreads, smem, stream>>>(xp, p, 1, packed_bytes, lr);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)split;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(ctiles * split));
     cfg.blockDim = dim3(kDcThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = AD ? 2 : 1;                // beside the kernel that writes T
     return cudaLaunchKernelEx(&cfg, kern, xp, p, split, packed_bytes, lr);
 }
 
@@ -814,22 +818,24 @@ cudaError_t launch_s(const LinearParams& p, const LowRankEpi& lr, const void* X,
            fill_frac(tiles * split * 2) > fill_frac(tiles * split) + 0.1)
         split *= 2;
     const __half* xp = static_cast<const __half*>(X);
-    if (split == 1) {
+    if (split == 1 && !AD) {
         kern<<<(unsigned)tiles, kDcThreads, smem, stream>>>(xp, p, 1, packed_bytes, lr);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)split;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(tiles * split));
     cfg.blockDim = dim3(kDcThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = AD ? 2 : 1;                // beside the kernel that writes T
     return cudaLaunchKernelEx(&cfg, kern, xp, p, split, packed_bytes, lr);
 }
 

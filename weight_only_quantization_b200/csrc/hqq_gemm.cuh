@@ -497,6 +497,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float* xbuf = reinterpret_cast<float*>(smem);        // the other parts' sums
     const int win = ks > 1 && bn > kGmWindow ? kGmWindow : bn;
+    if (lr.T) wait_for_T();
     LowRankTile lt;
     lt.place(smem + (ks > 1 ? (uint32_t)win * kGmM * 4u : 0u),
              (uint32_t)S * (kGmABytes + sh.b_bytes) - (ks > 1 ? (uint32_t)win * kGmM * 4u : 0u));
@@ -640,7 +641,7 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     if (e != cudaSuccess) return e;
     const int64_t tiles = (features + kGmM - 1) / kGmM;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = 1;
@@ -650,8 +651,10 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     cfg.blockDim = dim3(kGmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = lr.T ? 2 : 1;              // beside the kernel that writes T
     return cudaLaunchKernelEx(&cfg, kern, map, prm, lr, sh);
 }
 

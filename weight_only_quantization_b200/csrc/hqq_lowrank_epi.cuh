@@ -13,6 +13,11 @@
 
 namespace hqq {
 
+// The kernel that adds the term starts before the one that writes T has ended
+// (programmatic dependent launch): it waits here before its first read of T, and
+// reads T from L2, where that kernel's writes are.
+__device__ __forceinline__ void wait_for_T() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct LowRankEpi {
     const float* T;          // NULL: no term
     const int32_t* index;    // NULL: adapter 0 for every token
@@ -72,7 +77,7 @@ __device__ __forceinline__ float lowrank_dot16(const float* t, const float2 (&b)
     float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(t) + i);
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(t) + i);
         acc = __ffma2_rn(make_float2(q.x, q.y), b[2 * i], acc);
         acc = __ffma2_rn(make_float2(q.z, q.w), b[2 * i + 1], acc);
     }
@@ -93,7 +98,7 @@ struct LowRankTile {
     int* adapter;
     float* rows;
     uint32_t room;           // bytes for rows
-    const float* t;          // row 0 of the staged tokens
+    const float* t;          // row 0 of the tokens in global memory, or NULL: staged
     __device__ __forceinline__ void place(uint8_t* mem, uint32_t bytes) {
         adapter = reinterpret_cast<int*>(mem);           // 16-byte aligned
         rows = reinterpret_cast<float*>(mem + 2048);     // up to 512 tokens
@@ -111,18 +116,18 @@ struct LowRankTile {
             const int64_t have = (M - m) * per;
             const int all = n * per < have ? n * per : (int)have;
             for (int i = tid; i < all; i += nt)
-                reinterpret_cast<float4*>(rows)[i] = __ldg(reinterpret_cast<const float4*>(t) + i);
-            t = rows;
+                reinterpret_cast<float4*>(rows)[i] = __ldcg(reinterpret_cast<const float4*>(t) + i);
+            t = nullptr;
         }
     }
     // sum of 16 products of the staged token i from rank j (the same for the warp)
     __device__ __forceinline__ float dot16(const LowRankEpi& e, int i, int j,
                                            const float2 (&b)[8]) const {
-        const float4* row = reinterpret_cast<const float4*>(t + (int64_t)i * e.ld + j);
+        const float4* row = reinterpret_cast<const float4*>((t ? t : rows) + (int64_t)i * e.ld + j);
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 x = row[q];
+            const float4 x = t ? __ldcg(row + q) : row[q];
             acc = __ffma2_rn(make_float2(x.x, x.y), b[2 * q], acc);
             acc = __ffma2_rn(make_float2(x.z, x.w), b[2 * q + 1], acc);
         }
