@@ -61,10 +61,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// x = hi + lo with both in tf32 (lo rounded: the rest is below 2^-22 |x|).
+// x = hi + lo with both in tf32, rounded to nearest by integer additions (the MMA
+// drops the bits below lo's): the rest is below 2^-22 |x|.  The conversion
+// instruction measured slower.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__fsub_rn(x, __uint_as_float(hi))));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(__fsub_rn(x, __uint_as_float(hi))) + 0x1000u;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -468,7 +470,7 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t byt
 // Grid: x = column tile * csize + cluster rank, y = adapter, z = chunks of 8 NT
 // ranks.  Tiles below tiles_a make dA from X and P, the others dB from dY and T.
 template <int NT>
-__global__ void __launch_bounds__(kFgThreads)
+__global__ void __launch_bounds__(kFgThreads, NT <= 4 ? 3 : 2)
 factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
     using G = FgGeo<NT>;
     constexpr int RC = G::RC;
@@ -490,26 +492,36 @@ factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
     const int64_t chunks = (last - first + kFgTokens - 1) / kFgTokens;
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(fg_smem);
 
-    // stage s: [64 tokens][kFgZ] fp16 columns, then [64 tokens][SS] fp32
+    // stage s: [64 tokens][kFgZ] fp16 columns, then [64 tokens][SS] fp32; a thread's
+    // 16-byte pieces are one column of every ZR-th (SR-th) token
+    constexpr int ZG = kFgCols / 8, SG = RC / 4, ZR = kFgThreads / ZG, SR = kFgThreads / SG;
+    const int zr = tid / ZG, zq = tid % ZG, sr = tid / SG, sq = tid % SG;
+    const bool zin = c0 + 8 * zq < cols, sin = j0 + 4 * sq < p.ld;
+    const __half* zsrc = Z + c0 + 8 * zq;
+    const float* ssrc = S + j0 + 4 * sq;
+    const uint32_t zdst = smem + (uint32_t)(zr * kFgZ * 2 + zq * 16);
+    const uint32_t sdst = smem + (uint32_t)(kFgTokens * kFgZ * 2 + sr * G::SS * 4 + sq * 16);
+    const int total = (int)(last - first);
+    const int32_t* list = p.order ? p.order + first : nullptr;
     auto fill = [&](int64_t c, int s) {
         if (c < chunks) {
-            const uint32_t base = smem + (uint32_t)(s * G::STAGE);
-            constexpr int ZG = kFgCols / 8, SG = RC / 4;             // granules per row
-            for (int i = tid; i < kFgTokens * ZG; i += kFgThreads) {
-                const int r = i / ZG, q = i % ZG;
-                const int64_t l = first + c * kFgTokens + r, col = c0 + 8 * q;
-                const bool in = l < last && col < cols;
-                const int64_t m = in ? (p.order ? (int64_t)__ldg(p.order + l) : l) : 0;
-                cp16(base + (uint32_t)(r * kFgZ * 2 + q * 16), in ? Z + m * ldz + col : Z, in ? 16u : 0u);
+            const uint32_t stage = (uint32_t)(s * G::STAGE);
+            const int l0 = (int)c * kFgTokens;
+#pragma unroll
+            for (int u = 0; u < kFgTokens / ZR; ++u) {
+                const int l = l0 + zr + u * ZR;
+                const bool in = zin && l < total;
+                const int64_t m = in ? (list ? __ldg(list + l) : l) : 0;
+                cp16(zdst + stage + (uint32_t)(u * ZR * kFgZ * 2), in ? zsrc + m * ldz : Z, in ? 16u : 0u);
             }
-            for (int i = tid; i < kFgTokens * SG; i += kFgThreads) {
-                const int r = i / SG, q = i % SG;
-                const int64_t l = first + c * kFgTokens + r;
-                const int j = j0 + 4 * q;
-                const bool in = l < last && j < p.ld;
-                const int64_t m = in ? (p.order ? (int64_t)__ldg(p.order + l) : l) : 0;
-                cp16(base + (uint32_t)(kFgTokens * kFgZ * 2 + r * G::SS * 4 + q * 16),
-                     in ? S + m * p.ld + j : S, in ? 16u : 0u);
+#pragma unroll
+            for (int u = 0; u < (kFgTokens + SR - 1) / SR; ++u) {
+                const int l = l0 + sr + u * SR;
+                const bool in = sin && l < total;
+                const int64_t m = in ? (list ? __ldg(list + l) : l) : 0;
+                if (SR <= kFgTokens || sr < kFgTokens)
+                    cp16(sdst + stage + (uint32_t)(u * SR * G::SS * 4), in ? ssrc + m * p.ld : S,
+                         in ? 16u : 0u);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

@@ -8,16 +8,20 @@
 //   loss = w sum_k p_k (log p_k - log softmax(z)[index_k]);
 //   grad[v] = (w / t) (sum_k p_k  softmax(z)[v] - sum_{k: index_k = v} p_k).
 //
-// One cluster of C CTAs (C = 1 for up to 32768 16-bit logits) owns a token: the
-// row is read once into registers, each thread keeps a running maximum and sum
-// of exponentials, the pairs are joined by shuffles, shared memory and (C > 1)
-// distributed shared memory, and the gradient is formed from the same
-// registers, so a pass moves V elements in and V out and is bound by HBM.
-// Rows too long for eight CTAs' registers are read a second time instead.
-// The K entries are handled beside the dense row: one warp computes p, and after
-// the dense gradient is stored each distinct index is overwritten with the full
-// expression (one rounding to the output type; duplicates are summed in entry
-// order, so results do not depend on any execution order).
+// One cluster of C CTAs owns a token.  A CTA's share of the row (up to 64 KiB, three
+// CTAs per SM) is brought into shared memory by one bulk copy, so the copies of
+// one token run beside the arithmetic of the others on the SM; two passes over it
+// follow: running maximum and sum of exponentials (joined by shuffles, shared
+// memory and, C > 1, distributed shared memory), then the gradient.  A pass moves
+// V elements in and V out: the bound is HBM, with the exponentials' instructions
+// (about 9 an element) close behind.  Rows longer than eight CTAs' shared memory
+// are read a second time instead.  Rows off 16 bytes are handled as the aligned
+// 16-byte packs that cover them, the elements outside masked.
+// The K entries are handled beside the dense row: a thread takes an entry's value
+// and the student's logit, and after the dense gradient is stored each distinct
+// index is overwritten with the full expression (one rounding to the output type;
+// duplicates are summed in entry order, so results do not depend on any
+// execution order).
 // All arithmetic is in fp32; exponentials are ex2.approx of (z - max) log2(e)/t,
 // formed from the exact difference so that rows of equal values of any size
 // (masks at a type's lowest value) stay finite.
@@ -26,7 +30,7 @@
 
 #include <type_traits>
 
-#include "hqq_params.cuh"
+#include "hqq_tcgen05.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -34,9 +38,11 @@ namespace hqq {
 
 namespace {
 
-constexpr int kDsThreads = 512;
+constexpr int kDsThreads = 256;
 constexpr int kDsWarps = kDsThreads / 32;
 constexpr int kDsMaxCluster = 8;
+constexpr int kDsTries = 1000;                  // of the wait for the row before it is timed
+constexpr int64_t kDsMaxShare = 196608;          // bytes of a row kept by one CTA
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -53,42 +59,12 @@ template <> __device__ __forceinline__ float from_float(float v) { return v; }
 template <> __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 
-// W consecutive values of a row: 16 bytes, or one element.
-template <typename T, int W>
-struct alignas(sizeof(T) * W) Pack {
+// 16 bytes of a row.
+template <typename T>
+struct alignas(16) Pack {
+    static constexpr int W = 16 / (int)sizeof(T);
     T v[W];
 };
-
-template <typename T, int W>
-__device__ __forceinline__ Pack<T, W> load_pack(const T* p) {
-    Pack<T, W> r;
-    if constexpr (sizeof(T) * W == 16) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-        r = *reinterpret_cast<const Pack<T, W>*>(&u);
-    } else {
-        r.v[0] = *p;
-    }
-    return r;
-}
-
-template <typename T, int W>
-__device__ __forceinline__ void store_pack(T* p, const Pack<T, W>& r) {
-    if constexpr (sizeof(T) * W == 16)
-        __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&r));
-    else
-        *p = r.v[0];
-}
-
-// Pack i of a row of V values: the last one may be partial (-inf beyond V).
-template <typename T, int W>
-__device__ __forceinline__ Pack<T, W> row_pack(const T* row, int64_t i, int64_t V) {
-    if (W == 1 || (i + 1) * W <= V) return load_pack<T, W>(row + i * W);
-    Pack<T, W> r;
-#pragma unroll
-    for (int e = 0; e < W; ++e)
-        r.v[e] = i * W + e < V ? row[i * W + e] : from_float<T>(-INFINITY);
-    return r;
-}
 
 // The joined (maximum, sum of exponentials relative to it) of the warp's lanes,
 // in a fixed order; lanes without values hold (-inf, 0).  A maximum of -inf
@@ -105,31 +81,27 @@ __device__ __forceinline__ void join_lanes(float& m, float& s, float c) {
 }
 
 // The exponentials of a pack relative to m: e[i] = 2^((z_i - m) c).
-template <typename T, int W>
-__device__ __forceinline__ void exps(const Pack<T, W>& z, float m, float c, float2 (&e)[(W + 1) / 2]) {
-    if constexpr (W == 1) {
-        e[0].x = ex2(__fmul_rn(__fsub_rn(as_float(z.v[0]), m), c));
-        e[0].y = 0.0f;
-    } else {
+template <typename T>
+__device__ __forceinline__ void exps(const Pack<T>& z, float m, float c, float2 (&e)[Pack<T>::W / 2]) {
 #pragma unroll
-        for (int i = 0; i < W; i += 2) {
-            const float2 d = __fmul2_rn(
-                __fadd2_rn(make_float2(as_float(z.v[i]), as_float(z.v[i + 1])), make_float2(-m, -m)),
-                make_float2(c, c));
-            e[i / 2] = make_float2(ex2(d.x), ex2(d.y));
-        }
+    for (int i = 0; i < Pack<T>::W; i += 2) {
+        const float2 d = __fmul2_rn(
+            __fadd2_rn(make_float2(as_float(z.v[i]), as_float(z.v[i + 1])), make_float2(-m, -m)),
+            make_float2(c, c));
+        e[i / 2] = make_float2(ex2(d.x), ex2(d.y));
     }
 }
 
 // The largest value of N packs (NaN is passed over: it shows in the sum).
-template <typename T, int W, int N>
-__device__ __forceinline__ float pack_max(const Pack<T, W> (&z)[N]) {
-    if constexpr (W == 1 || sizeof(T) == 4) {
-        float mx = as_float(z[0].v[0]);
+template <typename T, int N>
+__device__ __forceinline__ float pack_max(const Pack<T> (&z)[N]) {
+    constexpr int W = Pack<T>::W;
+    if constexpr (sizeof(T) == 4) {
+        float mx = z[0].v[0];
 #pragma unroll
         for (int u = 0; u < N; ++u)
 #pragma unroll
-            for (int e = 0; e < W; ++e) mx = fmaxf(mx, as_float(z[u].v[e]));
+            for (int e = 0; e < W; ++e) mx = fmaxf(mx, z[u].v[e]);
         return mx;
     } else {                                             // two 16-bit values an operation
         using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
@@ -145,17 +117,17 @@ __device__ __forceinline__ float pack_max(const Pack<T, W> (&z)[N]) {
 }
 
 // Running maximum and sum of a thread, N packs further.
-template <typename T, int W, int N>
-__device__ __forceinline__ void local_stats(const Pack<T, W> (&z)[N], float c, float& m, float& s) {
+template <typename T, int N>
+__device__ __forceinline__ void local_stats(const Pack<T> (&z)[N], float c, float& m, float& s) {
     const float mx = fmaxf(m, pack_max(z));
     const float base = mx == -INFINITY ? 0.0f : mx;
     float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-        float2 e[(W + 1) / 2];
+        float2 e[Pack<T>::W / 2];
         exps(z[u], base, c, e);
 #pragma unroll
-        for (int i = 0; i < (W + 1) / 2; ++i) acc = __fadd2_rn(acc, e[i]);
+        for (int i = 0; i < Pack<T>::W / 2; ++i) acc = __fadd2_rn(acc, e[i]);
     }
     const float sum = __fadd_rn(acc.x, acc.y);
     // what came before (m, s), relative to the new maximum
@@ -179,15 +151,22 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Grid: one cluster of `csize` CTAs per token.  CACHED: the CTA's share of the
-// row is at most kDsThreads * NV packs and stays in registers.
-template <typename T, int W, int NV, bool CACHED>
-__global__ void __launch_bounds__(kDsThreads, 2)
-distill_kernel(const __grid_constant__ DistillParams p, int csize) {
-    __shared__ float st[kDistillMaxTop], sz[kDistillMaxTop];   // teacher value, student logit
-    __shared__ int4 si4[kDistillMaxTop / 4];                   // index, or -1
+// row (at most share_packs packs) is kept in shared memory.
+template <typename T, bool CACHED>
+__global__ void __launch_bounds__(kDsThreads, 3)
+distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_packs) {
+    constexpr int W = Pack<T>::W;
+    extern __shared__ __align__(16) uint8_t ds_smem[];
     __shared__ float wm[kDsWarps], ws[kDsWarps], tm_w[kDsWarps], ts_w[kDsWarps], loss_w[kDsWarps];
     __shared__ float cm[kDsMaxCluster], cs[kDsMaxCluster];
+    __shared__ uint64_t bar;
+    __shared__ int abort_flag;
+    const Pack<T>* cache = reinterpret_cast<const Pack<T>*>(ds_smem);
+    // the teacher's entries behind the row: index (or -1), value, student's logit
+    int4* si4 = reinterpret_cast<int4*>(ds_smem + (CACHED ? (size_t)share_packs * 16 : 0));
     int* si = reinterpret_cast<int*>(si4);
+    float* st = reinterpret_cast<float*>(si4 + (p.K + 3) / 4);
+    float* sz = st + p.K;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = csize == 1 ? 0 : (int)(blockIdx.x % (unsigned)csize);
@@ -196,19 +175,32 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
     T* grow = p.grad ? static_cast<T*>(p.grad) + tok * p.grad_stride : nullptr;
     const float w = p.weight ? p.weight[tok] : 1.0f;
     const float c = p.log2e_t;                           // log2(e) / t
-    const int64_t packs = (p.V + W - 1) / W;
-    const int64_t lo = packs * rank / csize, hi = packs * (rank + 1) / csize;
+    // the aligned packs that cover the row: `head` elements before it in the first
+    const int head = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row - head);
+    const int64_t np = (p.V + head + W - 1) / W;
+    const int64_t lo = np * rank / csize, hi = np * (rank + 1) / csize;
+    // the row's elements [first, end) that this CTA owns
+    const int64_t seg0 = lo == 0 ? 0 : lo * W - head, seg1 = hi == np ? p.V : hi * W - head;
+    // gradient rows of the same alignment are stored in whole packs
+    const bool whole = grow && (reinterpret_cast<uintptr_t>(grow) & 15u) / sizeof(T) == (unsigned)head;
+    auto store = [&](int64_t i, const Pack<T>& q) {      // pack i of the gradient
+        const int64_t e0 = i * W - head;
+        if (whole && e0 >= 0 && e0 + W <= p.V) {
+            __stcs(reinterpret_cast<uint4*>(grow + e0), *reinterpret_cast<const uint4*>(&q));
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (e0 + e >= 0 && e0 + e < p.V) grow[e0 + e] = q.v[e];
+        }
+    };
 
     if (w == 0.0f) {                                     // (every CTA of the cluster)
         if (grow) {
-            Pack<T, W> zero;
+            Pack<T> zero;
 #pragma unroll
             for (int e = 0; e < W; ++e) zero.v[e] = from_float<T>(0.0f);
-            for (int64_t i = lo + tid; i < hi; i += kDsThreads) {
-                if (W == 1 || (i + 1) * W <= p.V) store_pack<T, W>(grow + i * W, zero);
-                else
-                    for (int e = 0; i * W + e < p.V; ++e) grow[i * W + e] = zero.v[e];
-            }
+            for (int64_t i = lo + tid; i < hi; i += kDsThreads) store(i, zero);
         }
         if (rank == 0 && tid == 0) {
             if (p.loss) p.loss[tok] = 0.0f;
@@ -218,26 +210,42 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
     }
     if (csize > 1)                                       // every CTA has started (waited below)
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-
-    Pack<T, W> z[NV];
-    auto load_round = [&](int64_t i0) {
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int64_t i = i0 + (int64_t)u * kDsThreads;
-            if (i < hi) {
-                z[u] = row_pack<T, W>(row, i, p.V);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) z[u].v[e] = from_float<T>(-INFINITY);
-            }
+    if constexpr (CACHED) {
+        if (tid == 0) {
+            abort_flag = 0;
+            mbar_init(smem_u32(&bar), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            const uint32_t bytes = (uint32_t)(hi - lo) * 16u;
+            mbar_expect_tx(smem_u32(&bar), bytes);
+            if (bytes)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+                        "r"(smem_u32(ds_smem)), "l"(packs + lo), "r"(bytes), "r"(smem_u32(&bar))
+                    : "memory");
         }
+        __syncthreads();                                 // (the barrier is there to wait on)
+    }
+    // pack i of the row, elements outside it -inf
+    auto load = [&](int64_t i) {
+        Pack<T> q;
+        if constexpr (CACHED) {
+            q = cache[i - lo];
+        } else {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(packs + i));
+            q = *reinterpret_cast<const Pack<T>*>(&u);
+        }
+        if (i == 0 || i == np - 1) {
+            const int64_t e0 = i * W - head;
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (e0 + e < 0 || e0 + e >= p.V) q.v[e] = from_float<T>(-INFINITY);
+        }
+        return q;
     };
-    if constexpr (CACHED) load_round(lo + tid);          // in flight behind the entries' loads
 
-    // ---- the teacher's entries, one a thread (two from 512 entries on): value,
+    // ---- the teacher's entries, one a thread and round: value,
     // index and the student's logit there (rank 0 needs all of them for the loss,
     // the others their own segment's), (maximum, sum) as for the row
-    const int64_t seg0 = lo * W, seg1 = hi * W;
     float tm = -INFINITY, ts = 0.0f;
     for (int k = tid; k < p.K; k += kDsThreads) {
         const int64_t at = p.at64 ? static_cast<const int64_t*>(p.at)[tok * p.K + k]
@@ -255,15 +263,26 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
     }
     if (tid < 4 && p.K + tid < ((p.K + 3) & ~3)) si[p.K + tid] = -1;   // the last int4
 
-    // ---- maximum and sum of exponentials of the row
+    // ---- maximum and sum of exponentials of the row, four packs at a time
     float m = -INFINITY, s = 0.0f;
     if constexpr (CACHED) {
-        local_stats(z, c, m, s);
-    } else {
-        for (int64_t i0 = lo + tid; i0 < hi; i0 += (int64_t)NV * kDsThreads) {
-            load_round(i0);
-            local_stats(z, c, m, s);
+        bool landed = false;
+        for (int i = 0; i < kDsTries && !landed; ++i) landed = mbar_try(smem_u32(&bar), 0u);
+        if (!landed) mbar_wait(smem_u32(&bar), 0u, &abort_flag, nullptr, true);
+    }
+    for (int64_t i0 = lo + tid; i0 < hi; i0 += 4 * kDsThreads) {
+        Pack<T> z[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * kDsThreads;
+            if (i < hi) {
+                z[u] = load(i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) z[u].v[e] = from_float<T>(-INFINITY);
+            }
         }
+        local_stats(z, c, m, s);
     }
     join_lanes<32>(m, s, c);
     if (warp * 32 < p.K) join_lanes<32>(tm, ts, c);
@@ -325,32 +344,18 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
     const float wt = __fmul_rn(w, p.inv_t);
     if (grow) {
         const float coef = __fdiv_rn(__fmul_rn(wt, psum), s);
-        for (int64_t i0 = lo + tid; i0 < hi; i0 += (int64_t)NV * kDsThreads) {
+#pragma unroll 2
+        for (int64_t i = lo + tid; i < hi; i += kDsThreads) {
+            Pack<T> q = load(i);
+            float2 e[W / 2];
+            exps(q, m, c, e);
 #pragma unroll
-            for (int u = 0; u < NV; ++u) {
-                const int64_t i = i0 + (int64_t)u * kDsThreads;
-                if (i < hi) {
-                    Pack<T, W> q;
-                    float2 e[(W + 1) / 2];
-                    if constexpr (CACHED) q = z[u];
-                    else q = row_pack<T, W>(row, i, p.V);
-                    exps(q, m, c, e);
-#pragma unroll
-                    for (int j = 0; j < (W + 1) / 2; ++j) {
-                        e[j] = __fmul2_rn(e[j], make_float2(coef, coef));
-                        q.v[2 * j] = from_float<T>(e[j].x);
-                        if constexpr (W > 1) q.v[2 * j + 1] = from_float<T>(e[j].y);
-                    }
-                    if (W == 1 || (i + 1) * W <= p.V) {
-                        store_pack<T, W>(grow + i * W, q);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            if (i * W + j < p.V) grow[i * W + j] = q.v[j];
-                    }
-                }
+            for (int j = 0; j < W / 2; ++j) {
+                e[j] = __fmul2_rn(e[j], make_float2(coef, coef));
+                q.v[2 * j] = from_float<T>(e[j].x);
+                q.v[2 * j + 1] = from_float<T>(e[j].y);
             }
-            if constexpr (CACHED) break;
+            store(i, q);
         }
     }
     __syncthreads();                                     // the dense row is stored
@@ -387,13 +392,14 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize) {
     }
 }
 
-template <typename T, int W, int NV, bool CACHED>
-cudaError_t launch_ds(const DistillParams& p, int csize, cudaStream_t stream) {
-    auto kern = distill_kernel<T, W, NV, CACHED>;
-    if (csize == 1) {
-        kern<<<(unsigned)p.T, kDsThreads, 0, stream>>>(p, 1);
-        return cudaGetLastError();
-    }
+template <typename T, bool CACHED>
+cudaError_t launch_ds(const DistillParams& p, int csize, int share_packs, cudaStream_t stream) {
+    auto kern = distill_kernel<T, CACHED>;
+    const size_t smem = (CACHED ? (size_t)share_packs * 16 : 0) + (size_t)((p.K + 3) / 4) * 16 +
+                        (size_t)p.K * 8;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -402,36 +408,30 @@ cudaError_t launch_ds(const DistillParams& p, int csize, cudaStream_t stream) {
     attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(p.T * csize));
     cfg.blockDim = dim3(kDsThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, csize);
-}
-
-template <typename T, int W, int NV>
-cudaError_t launch_w(const DistillParams& p, cudaStream_t stream) {
-    constexpr int64_t kCap = (int64_t)kDsThreads * NV * W;      // values a CTA caches
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    int csize = 1;
-    // (a share is at most ceil(packs / csize) packs)
-    while (csize < kDsMaxCluster && csize * kCap < p.V) csize *= 2;
-    // few tokens: more CTAs per row while the grid is short of one per SM and
-    // every thread keeps two packs
-    while (csize < kDsMaxCluster && p.T * csize * 2 <= sms && p.V >= (int64_t)4 * csize * kDsThreads * W)
-        csize *= 2;
-    return csize * kCap >= p.V ? launch_ds<T, W, NV, true>(p, csize, stream)
-                               : launch_ds<T, W, NV, false>(p, csize, stream);
+    cfg.numAttrs = csize > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, csize, share_packs);
 }
 
 template <typename T>
 cudaError_t launch_t(const DistillParams& p, cudaStream_t stream) {
-    constexpr int W = 16 / (int)sizeof(T);
-    const bool vec = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.logits_stride % W == 0 &&
-                     (!p.grad || ((reinterpret_cast<uintptr_t>(p.grad) & 15u) == 0 &&
-                                  p.grad_stride % W == 0));
-    return vec ? launch_w<T, W, 8>(p, stream) : launch_w<T, 1, 32>(p, stream);
+    constexpr int64_t W = Pack<T>::W;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t np = (p.V + 2 * W - 2) / W;            // packs of a row of any alignment
+    int csize = 1;
+    // a share of 64 KiB at most (three CTAs per SM) while the cluster allows it
+    while (csize < kDsMaxCluster && (np + csize - 1) / csize > 65536 / 16) csize *= 2;
+    // few tokens: more CTAs per row while the grid is short of one per SM and
+    // every thread keeps two packs
+    while (csize < kDsMaxCluster && p.T * csize * 2 <= sms && np >= (int64_t)4 * csize * kDsThreads)
+        csize *= 2;
+    const int64_t share = np / csize + 1;
+    return share * 16 <= kDsMaxShare ? launch_ds<T, true>(p, csize, (int)share, stream)
+                                     : launch_ds<T, false>(p, csize, 0, stream);
 }
 
 }  // namespace
