@@ -566,6 +566,8 @@ extern "C" int hqq_distill(const void* logits, int64_t logits_stride, int dtype,
     p.K = (int)top_k;
     p.top_dtype = top_dtype;
     p.at64 = index_bytes == 8;
+    p.hash_mask = 63;
+    while (p.hash_mask < 2 * (int)top_k - 1) p.hash_mask = 2 * p.hash_mask + 1;
     p.inv_t = 1.0f / temperature;
     p.log2e_t = (float)(1.4426950408889634 / (double)temperature);
     const cudaError_t err = launch_distill(p, dtype, static_cast<cudaStream_t>(stream));

@@ -160,13 +160,13 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     __shared__ float wm[kDsWarps], ws[kDsWarps], tm_w[kDsWarps], ts_w[kDsWarps], loss_w[kDsWarps];
     __shared__ float cm[kDsMaxCluster], cs[kDsMaxCluster];
     __shared__ uint64_t bar;
-    __shared__ int abort_flag;
-    const Pack<T>* cache = reinterpret_cast<const Pack<T>*>(ds_smem);
+    __shared__ int abort_flag, repeated;
+    Pack<T>* cache = reinterpret_cast<Pack<T>*>(ds_smem);
     // the teacher's entries behind the row: index (or -1), value, student's logit
-    int4* si4 = reinterpret_cast<int4*>(ds_smem + (CACHED ? (size_t)share_packs * 16 : 0));
-    int* si = reinterpret_cast<int*>(si4);
-    float* st = reinterpret_cast<float*>(si4 + (p.K + 3) / 4);
+    int* si = reinterpret_cast<int*>(ds_smem + (CACHED ? (size_t)share_packs * 16 : 0));
+    float* st = reinterpret_cast<float*>(si + p.K);
     float* sz = st + p.K;
+    int* seen = reinterpret_cast<int*>(sz + p.K);        // hash set of the indices
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = csize == 1 ? 0 : (int)(blockIdx.x % (unsigned)csize);
@@ -178,21 +178,27 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     // the aligned packs that cover the row: `head` elements before it in the first
     const int head = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
     const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row - head);
-    const int64_t np = (p.V + head + W - 1) / W;
-    const int64_t lo = np * rank / csize, hi = np * (rank + 1) / csize;
-    // the row's elements [first, end) that this CTA owns
-    const int64_t seg0 = lo == 0 ? 0 : lo * W - head, seg1 = hi == np ? p.V : hi * W - head;
+    // (below 2^31 elements: counts of packs fit 32 bits)
+    const int np = (int)((p.V + head + W - 1) / W);
+    const int lo = (int)((int64_t)np * rank / csize), hi = (int)((int64_t)np * (rank + 1) / csize);
+    // the row's elements [seg0, seg1) that this CTA owns
+    const int64_t seg0 = lo == 0 ? 0 : (int64_t)lo * W - head;
+    const int64_t seg1 = hi == np ? p.V : (int64_t)hi * W - head;
+    // packs wholly inside the row; the others are the owning threads' extra work
+    const int in0 = lo == 0 && head ? 1 : lo;
+    const int in1 = hi == np && (p.V + head) % W ? hi - 1 : hi;
     // gradient rows of the same alignment are stored in whole packs
     const bool whole = grow && (reinterpret_cast<uintptr_t>(grow) & 15u) / sizeof(T) == (unsigned)head;
-    auto store = [&](int64_t i, const Pack<T>& q) {      // pack i of the gradient
-        const int64_t e0 = i * W - head;
-        if (whole && e0 >= 0 && e0 + W <= p.V) {
-            __stcs(reinterpret_cast<uint4*>(grow + e0), *reinterpret_cast<const uint4*>(&q));
-        } else {
+    uint4* gpacks = reinterpret_cast<uint4*>(grow - head);
+    auto store_each = [&](int i, const Pack<T>& q) {     // pack i, elements of the row alone
+        const int64_t e0 = (int64_t)i * W - head;
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (e0 + e >= 0 && e0 + e < p.V) grow[e0 + e] = q.v[e];
-        }
+        for (int e = 0; e < W; ++e)
+            if (e0 + e >= 0 && e0 + e < p.V) grow[e0 + e] = q.v[e];
+    };
+    auto store = [&](int i, const Pack<T>& q) {
+        if (whole && i >= in0 && i < in1) __stcs(gpacks + i, *reinterpret_cast<const uint4*>(&q));
+        else store_each(i, q);
     };
 
     if (w == 0.0f) {                                     // (every CTA of the cluster)
@@ -200,7 +206,7 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
             Pack<T> zero;
 #pragma unroll
             for (int e = 0; e < W; ++e) zero.v[e] = from_float<T>(0.0f);
-            for (int64_t i = lo + tid; i < hi; i += kDsThreads) store(i, zero);
+            for (int i = lo + tid; i < hi; i += kDsThreads) store(i, zero);
         }
         if (rank == 0 && tid == 0) {
             if (p.loss) p.loss[tok] = 0.0f;
@@ -210,9 +216,10 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     }
     if (csize > 1)                                       // every CTA has started (waited below)
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    if constexpr (CACHED) {
-        if (tid == 0) {
-            abort_flag = 0;
+    if (tid == 0) {
+        abort_flag = 0;
+        repeated = 0;
+        if constexpr (CACHED) {
             mbar_init(smem_u32(&bar), 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             const uint32_t bytes = (uint32_t)(hi - lo) * 16u;
@@ -223,24 +230,25 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
                         "r"(smem_u32(ds_smem)), "l"(packs + lo), "r"(bytes), "r"(smem_u32(&bar))
                     : "memory");
         }
-        __syncthreads();                                 // (the barrier is there to wait on)
     }
-    // pack i of the row, elements outside it -inf
-    auto load = [&](int64_t i) {
-        Pack<T> q;
+    for (int i = tid; i <= p.hash_mask; i += kDsThreads) seen[i] = -1;
+    __syncthreads();                                     // barrier and hash set are ready
+    // pack i with the elements outside the row -inf
+    auto masked = [&](int i, Pack<T> q) {
+        const int64_t e0 = (int64_t)i * W - head;
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e0 + e < 0 || e0 + e >= p.V) q.v[e] = from_float<T>(-INFINITY);
+        return q;
+    };
+    auto load = [&](int i) {
         if constexpr (CACHED) {
-            q = cache[i - lo];
+            return cache[i - lo];                        // (masked there once)
         } else {
             const uint4 u = __ldcs(reinterpret_cast<const uint4*>(packs + i));
-            q = *reinterpret_cast<const Pack<T>*>(&u);
+            const Pack<T> q = *reinterpret_cast<const Pack<T>*>(&u);
+            return i >= in0 && i < in1 ? q : masked(i, q);
         }
-        if (i == 0 || i == np - 1) {
-            const int64_t e0 = i * W - head;
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (e0 + e < 0 || e0 + e >= p.V) q.v[e] = from_float<T>(-INFINITY);
-        }
-        return q;
     };
 
     // ---- the teacher's entries, one a thread and round: value,
@@ -255,13 +263,24 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
         const float t = ok ? t0 : -INFINITY;
         si[k] = ok ? (int)at : -1;
         st[k] = t;
-        sz[k] = ok && (rank == 0 || (at >= seg0 && at < seg1)) ? as_float(row[at]) : 0.0f;
+        const bool mine = ok && at >= seg0 && at < seg1;
+        sz[k] = mine || (ok && rank == 0) ? as_float(row[at]) : 0.0f;
+        if (mine && grow) {                              // an index met twice?
+            uint32_t h = ((uint32_t)at * 2654435761u) >> 20;
+            for (int n = 0; n <= p.hash_mask; ++n, ++h) {
+                const int old = atomicCAS(seen + (h & (uint32_t)p.hash_mask), -1, (int)at);
+                if (old == -1) break;
+                if (old == (int)at) {
+                    repeated = 1;
+                    break;
+                }
+            }
+        }
         const float mx = fmaxf(tm, t), base = mx == -INFINITY ? 0.0f : mx;
         ts = __fadd_rn(__fmul_rn(ts, tm == -INFINITY ? 1.0f : ex2(__fmul_rn(__fsub_rn(tm, base), c))),
                        ex2(__fmul_rn(__fsub_rn(t, base), c)));
         tm = mx;
     }
-    if (tid < 4 && p.K + tid < ((p.K + 3) & ~3)) si[p.K + tid] = -1;   // the last int4
 
     // ---- maximum and sum of exponentials of the row, four packs at a time
     float m = -INFINITY, s = 0.0f;
@@ -270,18 +289,20 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
         for (int i = 0; i < kDsTries && !landed; ++i) landed = mbar_try(smem_u32(&bar), 0u);
         if (!landed) mbar_wait(smem_u32(&bar), 0u, &abort_flag, nullptr, true);
     }
-    for (int64_t i0 = lo + tid; i0 < hi; i0 += 4 * kDsThreads) {
+    if constexpr (CACHED) {
+        // the packs at the row's ends, by the threads that own them in both passes
+        if (in0 > lo && tid == 0) cache[0] = masked(lo, cache[0]);
+        if (in1 < hi && tid == (hi - 1 - lo) % kDsThreads) cache[hi - 1 - lo] = masked(hi - 1, cache[hi - 1 - lo]);
+    }
+    int i0 = lo + tid;
+    for (; i0 + 3 * kDsThreads < hi; i0 += 4 * kDsThreads) {
         Pack<T> z[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + u * kDsThreads;
-            if (i < hi) {
-                z[u] = load(i);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) z[u].v[e] = from_float<T>(-INFINITY);
-            }
-        }
+        for (int u = 0; u < 4; ++u) z[u] = load(i0 + u * kDsThreads);
+        local_stats(z, c, m, s);
+    }
+    for (; i0 < hi; i0 += kDsThreads) {
+        Pack<T> z[1] = {load(i0)};
         local_stats(z, c, m, s);
     }
     join_lanes<32>(m, s, c);
@@ -344,9 +365,7 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     const float wt = __fmul_rn(w, p.inv_t);
     if (grow) {
         const float coef = __fdiv_rn(__fmul_rn(wt, psum), s);
-#pragma unroll 2
-        for (int64_t i = lo + tid; i < hi; i += kDsThreads) {
-            Pack<T> q = load(i);
+        auto gradient = [&](Pack<T> q) {
             float2 e[W / 2];
             exps(q, m, c, e);
 #pragma unroll
@@ -355,7 +374,22 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
                 q.v[2 * j] = from_float<T>(e[j].x);
                 q.v[2 * j + 1] = from_float<T>(e[j].y);
             }
-            store(i, q);
+            return q;
+        };
+        if (whole) {
+            int i = lo + tid;
+            if (i < in0) {
+                store_each(i, gradient(load(i)));
+                i += kDsThreads;
+            }
+#pragma unroll 2
+            for (; i < in1; i += kDsThreads) {
+                const Pack<T> q = gradient(load(i));
+                __stcs(gpacks + i, *reinterpret_cast<const uint4*>(&q));
+            }
+            if (i < hi) store_each(i, gradient(load(i)));
+        } else {
+            for (int i = lo + tid; i < hi; i += kDsThreads) store_each(i, gradient(load(i)));
         }
     }
     __syncthreads();                                     // the dense row is stored
@@ -370,14 +404,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     for (int k = tid; k < p.K; k += kDsThreads) {
         const int at = si[k];
         if (at < seg0 || at >= seg1) continue;           // (unused entries: -1)
-        int same = 0;                                    // entries of this index
-#pragma unroll 4
-        for (int j = 0; j < (p.K + 3) / 4; ++j) {
-            const int4 o = si4[j];
-            same += (o.x == at) + (o.y == at) + (o.z == at) + (o.w == at);
-        }
         float mass = mass_of(k);
-        if (same > 1) {                                  // in entry order; the first writes
+        if (repeated) {                                  // in entry order; the first writes
             bool first = true;
             mass = 0.0f;
             for (int j = 0; j < p.K; ++j)
@@ -395,8 +423,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
 template <typename T, bool CACHED>
 cudaError_t launch_ds(const DistillParams& p, int csize, int share_packs, cudaStream_t stream) {
     auto kern = distill_kernel<T, CACHED>;
-    const size_t smem = (CACHED ? (size_t)share_packs * 16 : 0) + (size_t)((p.K + 3) / 4) * 16 +
-                        (size_t)p.K * 8;
+    const size_t smem = (CACHED ? (size_t)share_packs * 16 : 0) + (size_t)p.K * 12 +
+                        (size_t)(p.hash_mask + 1) * 4;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -68,6 +68,7 @@ struct DistillParams {
     float* lse;              // nullable [T]
     int64_t T, V, logits_stride, grad_stride;
     int K, top_dtype, at64;
+    int hash_mask;           // slots - 1 of the set of a token's indices: 2^k - 1 >= 2 K - 1
     float inv_t, log2e_t;    // 1 / t and log2(e) / t
 };
 
