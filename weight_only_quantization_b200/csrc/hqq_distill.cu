@@ -64,6 +64,28 @@ template <typename T>
 struct alignas(16) Pack {
     static constexpr int W = 16 / (int)sizeof(T);
     T v[W];
+    // values 2 i and 2 i + 1, converted a word at a time
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) {
+            return make_float2(v[2 * i], v[2 * i + 1]);
+        } else {
+            const uint32_t u = reinterpret_cast<const uint32_t*>(v)[i];
+            if constexpr (std::is_same<T, __half>::value)
+                return __half22float2(*reinterpret_cast<const __half2*>(&u));
+            else
+                return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        }
+    }
+    __device__ __forceinline__ void set_pair(int i, float2 x) {
+        if constexpr (sizeof(T) == 4) {
+            v[2 * i] = x.x;
+            v[2 * i + 1] = x.y;
+        } else if constexpr (std::is_same<T, __half>::value) {
+            reinterpret_cast<__half2*>(v)[i] = __floats2half2_rn(x.x, x.y);
+        } else {
+            reinterpret_cast<__nv_bfloat162*>(v)[i] = __floats2bfloat162_rn(x.x, x.y);
+        }
+    }
 };
 
 // The joined (maximum, sum of exponentials relative to it) of the warp's lanes,
@@ -84,11 +106,9 @@ __device__ __forceinline__ void join_lanes(float& m, float& s, float c) {
 template <typename T>
 __device__ __forceinline__ void exps(const Pack<T>& z, float m, float c, float2 (&e)[Pack<T>::W / 2]) {
 #pragma unroll
-    for (int i = 0; i < Pack<T>::W; i += 2) {
-        const float2 d = __fmul2_rn(
-            __fadd2_rn(make_float2(as_float(z.v[i]), as_float(z.v[i + 1])), make_float2(-m, -m)),
-            make_float2(c, c));
-        e[i / 2] = make_float2(ex2(d.x), ex2(d.y));
+    for (int i = 0; i < Pack<T>::W / 2; ++i) {
+        const float2 d = __fmul2_rn(__fadd2_rn(z.pair(i), make_float2(-m, -m)), make_float2(c, c));
+        e[i] = make_float2(ex2(d.x), ex2(d.y));
     }
 }
 
@@ -369,11 +389,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
             float2 e[W / 2];
             exps(q, m, c, e);
 #pragma unroll
-            for (int j = 0; j < W / 2; ++j) {
-                e[j] = __fmul2_rn(e[j], make_float2(coef, coef));
-                q.v[2 * j] = from_float<T>(e[j].x);
-                q.v[2 * j + 1] = from_float<T>(e[j].y);
-            }
+            for (int j = 0; j < W / 2; ++j)
+                q.set_pair(j, __fmul2_rn(e[j], make_float2(coef, coef)));
             return q;
         };
         if (whole) {
