@@ -85,6 +85,10 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 }
 
 // How a factor's values reach the B operand.
+// A kernel launched beside the one before it does not end before that one: what
+// waits for its end may rely on both.
+__device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 enum FactorForm {
     kKPairs,     // fp16, the reduction index contiguous: one 16-byte load a lane
     kJPairs,     // fp16, the rank contiguous: 8x8 blocks transposed in registers
@@ -361,6 +365,7 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
         }
         __syncthreads();                                 // red is written again
     }
+    if (p.beside) wait_for_prior();
 }
 
 template <FactorForm FORM, int NT>
@@ -376,24 +381,29 @@ cudaError_t launch_shrink_nt(const ShrinkParams& p, cudaStream_t stream) {
     int64_t slots = p.count < kShTokens ? p.count : kShTokens;
     if (p.M < slots) slots = p.M;
     while (slots > 1 && tiles * slots > 256) slots = (slots + 1) / 2;
-    // split the reduction while the grid stays within two CTAs per SM and every warp
-    // keeps two steps
+    // split the reduction while the busy CTAs stay within two per SM and every warp
+    // keeps two steps: up to 256 tokens every one may have an adapter of its own, more
+    // come as runs of a few
+    const int64_t pairs = p.M <= 256 ? (p.M < tiles * slots ? p.M : tiles * slots)
+                                     : tiles + (p.index ? p.count : 0);
     int csize = 1;
-    while (csize < kShMaxCluster && tiles * chunks * csize <= sms &&
+    while (csize < kShMaxCluster && pairs * chunks * csize <= sms &&
            blocks >= (int64_t)2 * csize * kShWarps)
         csize *= 2;
     auto kern = shrink_kernel<FORM, NT>;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)csize;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(tiles * slots * csize), (unsigned)chunks);
     cfg.blockDim = dim3(kShThreads);
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.beside ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p, csize, (int)slots);
 }
 
@@ -410,6 +420,7 @@ __global__ void __launch_bounds__(256)
 order_kernel(const int32_t* __restrict__ index, int64_t M, int count, int32_t* __restrict__ order,
              int32_t* __restrict__ start) {
     __shared__ int part[8], below[8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int a = (int)blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int less = 0;
     for (int64_t m = tid; m < M; m += 256) {
@@ -441,6 +452,7 @@ order_kernel(const int32_t* __restrict__ index, int64_t M, int count, int32_t* _
         __syncthreads();
     }
     if (tid == 0 && a == count - 1) start[count] = base;
+    wait_for_prior();
 }
 
 // ---- gradients of the factors ------------------------------------------------
@@ -481,14 +493,15 @@ factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
     const int tile = (int)(csize == 1 ? blockIdx.x : blockIdx.x / (unsigned)csize);
     // (the input gradient's kernel may start its own work)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_prior();                                    // T, P and the lists are there
     const int a = (int)blockIdx.y, j0 = (int)blockIdx.z * RC;
     const bool isA = tile < p.tiles_a;
     const __half* Z = isA ? p.X : p.dY;
     const int64_t ldz = isA ? p.ldx : p.ldy, cols = isA ? p.K : p.N;
     const float* S = isA ? p.P : p.T;
     const int64_t c0 = (int64_t)(isA ? tile : tile - p.tiles_a) * kFgCols;
-    const int64_t first = p.order ? p.start[a] : 0;
-    const int64_t last = p.order ? p.start[a + 1] : (a == 0 ? p.M : 0);
+    const int64_t first = p.order ? __ldcg(p.start + a) : 0;
+    const int64_t last = p.order ? __ldcg(p.start + a + 1) : (a == 0 ? p.M : 0);
     const int64_t chunks = (last - first + kFgTokens - 1) / kFgTokens;
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(fg_smem);
 
@@ -511,14 +524,14 @@ factor_grad_kernel(const __grid_constant__ FactorGradParams p, int csize) {
             for (int u = 0; u < kFgTokens / ZR; ++u) {
                 const int l = l0 + zr + u * ZR;
                 const bool in = zin && l < total;
-                const int64_t m = in ? (list ? __ldg(list + l) : l) : 0;
+                const int64_t m = in ? (list ? __ldcg(list + l) : l) : 0;
                 cp16(zdst + stage + (uint32_t)(u * ZR * kFgZ * 2), in ? zsrc + m * ldz : Z, in ? 16u : 0u);
             }
 #pragma unroll
             for (int u = 0; u < (kFgTokens + SR - 1) / SR; ++u) {
                 const int l = l0 + sr + u * SR;
                 const bool in = sin && l < total;
-                const int64_t m = in ? (list ? __ldg(list + l) : l) : 0;
+                const int64_t m = in ? (list ? __ldcg(list + l) : l) : 0;
                 if (SR <= kFgTokens || sr < kFgTokens)
                     cp16(sdst + stage + (uint32_t)(u * SR * G::SS * 4), in ? ssrc + m * p.ld : S,
                          in ? 16u : 0u);
@@ -650,17 +663,19 @@ cudaError_t launch_fg(const FactorGradParams& p, int tiles, cudaStream_t stream)
            p.M >= (int64_t)4 * csize * kFgTokens)
         csize *= 2;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)csize;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(tiles * csize), (unsigned)p.count, (unsigned)zc);
     cfg.blockDim = dim3(kFgThreads);
     cfg.dynamicSmemBytes = G::BYTES;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p, csize);
 }
 
@@ -696,8 +711,16 @@ cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
 
 cudaError_t launch_order(const int32_t* index, int64_t M, int count, int32_t* order,
                          int32_t* start, cudaStream_t stream) {
-    order_kernel<<<(unsigned)count, 256, 0, stream>>>(index, M, count, order, start);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)count);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, order_kernel, index, M, count, order, start);
 }
 
 cudaError_t launch_factor_grads(FactorGradParams p, cudaStream_t stream) {

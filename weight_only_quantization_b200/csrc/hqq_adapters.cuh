@@ -15,6 +15,7 @@ struct ShrinkParams {
     float* T;                 // [M, ld]
     int64_t M, K, ldx, sa, sk, sj;
     int ld, rank, count, dtype;
+    int beside;               // may run beside the kernel launched before it
 };
 
 // dA[a, j, k] and dB[a, n, j] from scaled P = dY B and T = X A^T.

@@ -817,6 +817,7 @@ extern "C" int hqq_linear_adapters_backward(const void* dY, const void* X, int64
             sh.sa = sB;
             sh.sk = rank;
             sh.sj = 1;
+            sh.beside = dB != nullptr;     // T's kernel, which started after all before it
             if (launch_shrink(sh, s) != cudaSuccess) return HQQ_ERR_CUDA;
         }
         if (dA || dB) {

@@ -734,7 +734,20 @@ decode_sx_kernel(const __half* __restrict__ X, const __grid_constant__ LinearPar
                     for (int e = 0; e < 4; ++e)
                         acc[c][e] += cred[((q - 1) * kDcWarps + warp) * TW + (4 * c + e) * 32 + lane];
     }
-    if constexpr (AD) wait_for_T();
+    if constexpr (AD) {
+        wait_for_T();
+        if (rank == 0) {
+            const int64_t f0 = n0 < p.N ? n0 : p.N - 1, f1 = n1 < p.N ? n1 : p.N - 1;
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 d = lowrank_pair(lr, 8 * c + 2 * j + h, p.M, f0, f1);
+                    acc[c][h] = __fadd_rn(acc[c][h], d.x);
+                    acc[c][2 + h] = __fadd_rn(acc[c][2 + h], d.y);
+                }
+        }
+    }
     if (rank == 0) {
 #pragma unroll
         for (int c = 0; c < NT; ++c)
@@ -742,10 +755,7 @@ decode_sx_kernel(const __half* __restrict__ X, const __grid_constant__ LinearPar
             for (int e = 0; e < 4; ++e) {
                 const int64_t n = tile * 16 + r + 8 * (e >> 1);
                 const int64_t m = 8 * c + 2 * j + (e & 1);
-                if (n < p.N && m < p.M) {
-                    if constexpr (AD) acc[c][e] = __fadd_rn(acc[c][e], lowrank_term(lr, m, n));
-                    p.Y[m * p.N + n] = __float2half_rn(acc[c][e]);
-                }
+                if (n < p.N && m < p.M) p.Y[m * p.N + n] = __float2half_rn(acc[c][e]);
             }
     }
 }

@@ -54,6 +54,7 @@ struct GemmShape {
     int stages, ks;
     uint32_t b_bytes;        // staged tokens of a CTA: bn / CG rows of 128 bytes
     int vec;                 // 32 codes are one aligned run in memory (4 bits)
+    int tile0;               // first feature tile of the launch
 };
 
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
@@ -163,6 +164,14 @@ __device__ __forceinline__ __half ldnc(const __half* p) {
     uint16_t v;
     asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return __ushort_as_half(v);
+}
+
+// One fp32 column of this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    return __uint_as_float(r);
 }
 
 // 32 codes of one row from a multiple of 32, as loaded: nothing done with a
@@ -300,7 +309,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
     const int ks = sh.ks, zr = (int)blockIdx.z;
     const uint32_t leader = CG * (uint32_t)zr;                     // cluster rank
     const int64_t m0 = (int64_t)(blockIdx.x / CG) * bn;
-    const int64_t n0 = ((int64_t)blockIdx.y * CG + c2) * kGmM;
+    const int64_t n0 = (sh.tile0 + (int64_t)blockIdx.y * CG + c2) * kGmM;
     const int64_t features = TRANS ? prm.K : prm.N;
     const int KT = (int)(((TRANS ? prm.N : prm.K) + kGmK - 1) / kGmK);
     const int kt0 = (int)((int64_t)KT * zr / ks);
@@ -533,6 +542,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
             regs.init();
 #pragma unroll 1
             for (int c = 8 * grp; c < share; c += 32) {
+                if (lr.T && !lt.uniform(c)) continue;    // (below)
                 float v[8];
                 tmem_ld8(trow + (uint32_t)(c0 + c), v);
                 for (int q = 0; q < ks - 1; ++q) {
@@ -547,6 +557,22 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
                     if (m < prm.M && nf < features) prm.Y[m * features + nf] = __float2half_rn(v[i]);
                 }
             }
+            // blocks of eight tokens with several adapters: two tokens for each of
+            // the four warps of a quarter (a token's factor loads are a latency each)
+            if (lr.T)
+#pragma unroll 1
+                for (int b = 0; b < share; b += 8) {
+                    if (lt.uniform(b)) continue;
+#pragma unroll 1
+                    for (int c = b + grp; c < b + 8; c += 4) {
+                        float v = tmem_ld1(trow + (uint32_t)(c0 + c));
+                        for (int q = 0; q < ks - 1; ++q)
+                            v = __fadd_rn(v, xbuf[((size_t)q * share + c) * kGmM + f]);
+                        v = __fadd_rn(v, lt.term(lr, regs, c, nfc));
+                        const int64_t m = m0 + c0 + c;
+                        if (m < prm.M && nf < features) prm.Y[m * features + nf] = __float2half_rn(v);
+                    }
+                }
         }
         __syncwarp();
     }
@@ -566,6 +592,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
 
 struct GemmPlan {
     int cg, ks, bn;
+    int64_t rows;            // rows of feature tiles (cg tiles each) that fill whole rounds
+    double cost, round;      // us: all of it, one round
 };
 
 // Tile choice, from the times of every (CG, ks, bn) on four matrices and 64 to
@@ -580,8 +608,7 @@ struct GemmPlan {
 // once (splits by 8 measured slower wherever more than 8 clusters were needed).
 GemmPlan plan_gemm(int64_t M, int64_t features, int64_t depth, int sms) {
     const int64_t steps = (depth + kGmK - 1) / kGmK, tiles = (features + kGmM - 1) / kGmM;
-    GemmPlan best = {1, 1, 16};
-    double cost = 1e30;
+    GemmPlan best = {1, 1, 16, 0, 1e30, 0.0};
     for (int cg = 1; cg <= 2; ++cg)
         for (int ks = 1; ks * cg <= 8; ks *= 2) {
             if (ks > 1 && steps < 4 * ks) break;
@@ -599,25 +626,27 @@ GemmPlan plan_gemm(int64_t M, int64_t features, int64_t depth, int sms) {
                 if (size == 8 && ctas > slots) break;
                 const double rounds = (double)((ctas + slots - 1) / slots);
                 const double step = cg == 1 ? 0.60 : 0.0019 * bn > 0.74 ? 0.0019 * bn : 0.74;
-                const double c = rounds * ((double)((steps + ks - 1) / ks) * step +
-                                           (cg == 1 ? 8.5 : 13.0) + (ks > 1 ? 0.02 : 0.01) * bn);
-                if (c < cost) {
-                    cost = c;
-                    best = {cg, ks, bn};
-                }
+                const double one = (double)((steps + ks - 1) / ks) * step +
+                                   (cg == 1 ? 8.5 : 13.0) + (ks > 1 ? 0.02 : 0.01) * bn;
+                if (rounds * one < best.cost)
+                    best = {cg, ks, bn, (ctas / slots) * slots / ((M + bn - 1) / bn * size),
+                            rounds * one, one};
                 if (bn <= 64 || bn % unit != 0) break;
             }
         }
     return best;
 }
 
+// Feature tiles tile0 .. tile0 + tiles - 1 (kGmM features each) of the output.
 template <int NBITS, bool SMALL, bool TRANS, int CG>
 cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const void* X, int64_t ld,
-                           const GemmPlan& plan, cudaStream_t stream) {
+                           const GemmPlan& plan, int64_t tile0, int64_t tiles, bool beside_T,
+                           cudaStream_t stream) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    const int64_t depth = TRANS ? prm.N : prm.K, features = TRANS ? prm.K : prm.N;
+    const int64_t depth = TRANS ? prm.N : prm.K;
     GemmShape sh;
+    sh.tile0 = (int)tile0;
     sh.bn = plan.bn;
     sh.nmma = plan.bn > 256 ? plan.bn / 2 : plan.bn;
     sh.ks = plan.ks;
@@ -639,7 +668,6 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     const size_t smem = 1024 + kGmStageBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (features + kGmM - 1) / kGmM;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -654,7 +682,7 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = lr.T ? 2 : 1;              // beside the kernel that writes T
+    cfg.numAttrs = beside_T ? 2 : 1;          // beside the kernel that writes T
     return cudaLaunchKernelEx(&cfg, kern, map, prm, lr, sh);
 }
 
@@ -664,9 +692,30 @@ cudaError_t launch_gemm_n(const LinearParams& prm, const LowRankEpi& lr, const v
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const GemmPlan plan = plan_gemm(prm.M, TRANS ? prm.K : prm.N, TRANS ? prm.N : prm.K, sms);
-    return plan.cg == 2 ? launch_gemm_cg<NBITS, SMALL, TRANS, 2>(prm, lr, X, ld, plan, stream)
-                        : launch_gemm_cg<NBITS, SMALL, TRANS, 1>(prm, lr, X, ld, plan, stream);
+    const int64_t features = TRANS ? prm.K : prm.N, depth = TRANS ? prm.N : prm.K;
+    const int64_t tiles = (features + kGmM - 1) / kGmM;
+    auto launch = [&](const GemmPlan& plan, int64_t tile0, int64_t count, bool beside_T) {
+        return plan.cg == 2
+            ? launch_gemm_cg<NBITS, SMALL, TRANS, 2>(prm, lr, X, ld, plan, tile0, count, beside_T, stream)
+            : launch_gemm_cg<NBITS, SMALL, TRANS, 1>(prm, lr, X, ld, plan, tile0, count, beside_T, stream);
+    };
+    const GemmPlan plan = plan_gemm(prm.M, features, depth, sms);
+    // A nearly empty last round is a launch of its own, with the tiles that suit
+    // what is left: the gate matrix at 2048 tokens is 448 pair tiles, 6 rounds of 74
+    // and 4 tiles over (a seventh round of 142 us; on their own about 30).
+    const int64_t whole = plan.rows * plan.cg;
+    if (whole > 0 && whole < tiles) {
+        const GemmPlan rest = plan_gemm(prm.M, features - whole * kGmM, depth, sms);
+        const int64_t per_row = (prm.M + plan.bn - 1) / plan.bn * plan.cg * plan.ks;
+        const int64_t size = plan.cg * plan.ks;
+        const int64_t slots = size == 4 ? sms * 16 / 18 / 4 * 4 : size == 2 ? sms / 2 * 2 : size == 1 ? sms : 64;
+        const double first = (double)((plan.rows * per_row + slots - 1) / slots) * plan.round;
+        if (first + rest.cost + 3.0 < plan.cost) {
+            const cudaError_t e = launch(plan, 0, whole, lr.T != nullptr);
+            return e == cudaSuccess ? launch(rest, whole, tiles - whole, false) : e;
+        }
+    }
+    return launch(plan, 0, tiles, lr.T != nullptr);
 }
 
 // X: [M, K] (TRANS: dY, [M, N]), rows ld values apart, 16-byte aligned.

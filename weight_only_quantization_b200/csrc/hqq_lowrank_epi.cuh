@@ -133,54 +133,50 @@ struct LowRankTile {
         }
         return __fadd_rn(acc.x, acc.y);
     }
-    // v[i] += the term of staged token c + i (i < 8) at feature f
-    __device__ __forceinline__ void add8(const LowRankEpi& e, LowRankRegs32& r, int c, int64_t f,
-                                         float (&v)[8]) const {
+    // whether staged tokens c .. c + 7 have one adapter (or none) in common
+    __device__ __forceinline__ bool uniform(int c) const {
         const int4 a0 = *reinterpret_cast<const int4*>(adapter + c);
         const int4 a1 = *reinterpret_cast<const int4*>(adapter + c + 4);
         const bool same = a0.y == a0.x && a0.z == a0.x && a0.w == a0.x && a1.x == a0.x &&
                           a1.y == a0.x && a1.z == a0.x && a1.w == a0.x;
-        if (same) {
-            if (a0.x < 0) return;
-            for (int j = 0; j < e.ld; j += 32) {
-                const bool two = j + 16 < e.ld;
-                if (r.a != a0.x || r.j0 != j) {
-                    lowrank_load16(e, a0.x, f, j, r.b[0]);
-                    if (two) lowrank_load16(e, a0.x, f, j + 16, r.b[1]);
-                    r.a = a0.x;
-                    r.j0 = j;
-                }
+        return same;
+    }
+    __device__ __forceinline__ void load(const LowRankEpi& e, LowRankRegs32& r, int a, int64_t f,
+                                         int j) const {
+        if (r.a != a || r.j0 != j) {
+            lowrank_load16(e, a, f, j, r.b[0]);
+            if (j + 16 < e.ld) lowrank_load16(e, a, f, j + 16, r.b[1]);
+            r.a = a;
+            r.j0 = j;
+        }
+    }
+    // v[i] += the term of staged token c + i (i < 8) at feature f; uniform(c) holds
+    __device__ __forceinline__ void add8(const LowRankEpi& e, LowRankRegs32& r, int c, int64_t f,
+                                         float (&v)[8]) const {
+        const int a = adapter[c];
+        if (a < 0) return;
+        for (int j = 0; j < e.ld; j += 32) {
+            const bool two = j + 16 < e.ld;
+            load(e, r, a, f, j);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = __fadd_rn(v[i], dot16(e, c + i, j, r.b[0]));
-                    if (two) v[i] = __fadd_rn(v[i], dot16(e, c + i, j + 16, r.b[1]));
-                }
+            for (int i = 0; i < 8; ++i) {
+                v[i] = __fadd_rn(v[i], dot16(e, c + i, j, r.b[0]));
+                if (two) v[i] = __fadd_rn(v[i], dot16(e, c + i, j + 16, r.b[1]));
             }
-            return;
         }
-        // tokens of several adapters: 16 ranks of one token a step, the next
-        // step's factor values loaded ahead
-        const int steps = e.ld >> 4, all = 8 * steps;
-        auto adapter_of = [&](int q) { return adapter[c + q / steps]; };
-        auto load = [&](int q, float2 (&b)[8]) {
-            if (q < all && adapter_of(q) >= 0)
-                lowrank_load16(e, adapter_of(q), f, 16 * (q % steps), b);
-        };
-        auto add = [&](int q, const float2 (&b)[8]) {
-            if (q >= all || adapter_of(q) < 0) return;
-            const float d = dot16(e, c + q / steps, 16 * (q % steps), b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i == q / steps ? __fadd_rn(v[i], d) : v[i];
-        };
-        load(0, r.b[0]);
-#pragma unroll 1
-        for (int q = 0; q < all; q += 2) {
-            load(q + 1, r.b[1]);
-            add(q, r.b[0]);
-            load(q + 2, r.b[0]);
-            add(q + 1, r.b[1]);
-        }
-        r.a = -1;
+    }
+    // the term of staged token c alone
+    __device__ __forceinline__ float term(const LowRankEpi& e, LowRankRegs32& r, int c,
+                                          int64_t f) const {
+        const int a = adapter[c];
+        float d = 0.0f;
+        if (a >= 0)
+            for (int j = 0; j < e.ld; j += 32) {
+                load(e, r, a, f, j);
+                d = __fadd_rn(d, dot16(e, c, j, r.b[0]));
+                if (j + 16 < e.ld) d = __fadd_rn(d, dot16(e, c, j + 16, r.b[1]));
+            }
+        return d;
     }
 };
 
@@ -197,6 +193,25 @@ __device__ __forceinline__ float lowrank_term(const LowRankEpi& e, int64_t m, in
             d = __fadd_rn(d, lowrank_dot16(e.T + m * e.ld + j, b));
         }
     return d;
+}
+
+// The terms of one token (clamped to M - 1) at two features, without branches, so
+// that the loads of several tokens are in flight together.
+__device__ __forceinline__ float2 lowrank_pair(const LowRankEpi& e, int64_t m, int64_t M, int64_t f0,
+                                               int64_t f1) {
+    const int64_t mc = m < M ? m : M - 1;
+    const int a = lowrank_adapter(e, mc), ac = a < 0 ? 0 : a;
+    float2 d = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+    for (int j = 0; j < e.ld; j += 16) {
+        float2 b0[8], b1[8];
+        lowrank_load16(e, ac, f0, j, b0);
+        lowrank_load16(e, ac, f1, j, b1);
+        d.x = __fadd_rn(d.x, lowrank_dot16(e.T + mc * e.ld + j, b0));
+        d.y = __fadd_rn(d.y, lowrank_dot16(e.T + mc * e.ld + j, b1));
+    }
+    // (a token without an adapter has read a row that nothing wrote)
+    return a < 0 ? make_float2(0.0f, 0.0f) : d;
 }
 
 }  // namespace hqq
