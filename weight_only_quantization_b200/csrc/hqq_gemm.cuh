@@ -55,6 +55,7 @@ struct GemmShape {
     uint32_t b_bytes;        // staged tokens of a CTA: bn / CG rows of 128 bytes
     int vec;                 // 32 codes are one aligned run in memory (4 bits)
     int tile0;               // first feature tile of the launch
+    int out_vec;             // the output's rows are whole aligned 16-byte runs
 };
 
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
@@ -164,6 +165,31 @@ __device__ __forceinline__ __half ldnc(const __half* p) {
     uint16_t v;
     asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return __ushort_as_half(v);
+}
+
+// Eight fp32 columns of this warp's 32 tensor-memory lanes in the layout of two
+// m16n8 MMA accumulators: v[h][e] = lane 16 h + lane / 4 + 8 (e / 2), column
+// 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][4]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr + (16u << 16)));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const float (&v)[2][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::
+                         "r"(taddr + ((uint32_t)(16 * h) << 16)),
+                     "r"(__float_as_uint(v[h][0])), "r"(__float_as_uint(v[h][1])),
+                     "r"(__float_as_uint(v[h][2])), "r"(__float_as_uint(v[h][3]))
+                     : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // One fp32 column of this warp's 32 tensor-memory lanes.
@@ -298,6 +324,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t bars[3 * kGmMaxStages + 1];
     __shared__ uint32_t tmem_holder;
+    __shared__ __align__(16) uint8_t stage_out[16][512];           // 8 tokens x 32 features a warp
     __shared__ int abort_flag;
     const int S = sh.stages, bn = sh.bn, parts = bn / sh.nmma;
     uint8_t* a_st = smem;
@@ -538,31 +565,72 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
         if (ks > 1) cluster_sync_all();
         else __syncthreads();
         if (epi) {
-            LowRankRegs32 regs;
-            regs.init();
+            // eight tokens at a time in the layout of an m16n8 MMA, stored through a
+            // transposition in shared memory: 64 bytes of a token's row for 4 lanes
+            LowRankFrag frag;
+            frag.init();
+            uint8_t* out = stage_out[warp - 2];
+            const uint32_t out_row = smem_u32(out) + (uint32_t)((lane & 7) * 64 + (lane >> 3) * 16);
+            const int64_t fb = n0 + 32 * (warp & 3);     // the warp's features
+            // (16 ranks a pass: the factor's values stay in registers, the sums go back
+            // to tensor memory between passes)
+            const int ranks = lr.T ? lr.ld : 16;
+#pragma unroll 1
+            for (int j = 0; j < ranks; j += 16, frag.init())
 #pragma unroll 1
             for (int c = 8 * grp; c < share; c += 32) {
-                if (lr.T && !lt.uniform(c)) continue;    // (below)
-                float v[8];
-                tmem_ld8(trow + (uint32_t)(c0 + c), v);
-                for (int q = 0; q < ks - 1; ++q) {
-                    const float* src = xbuf + (size_t)q * share * kGmM + f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], src[(c + i) * kGmM]);
+                if (lr.T && !lt.fast(c)) continue;       // (below)
+                float v[2][4];
+                tmem_ld_frag(trow + (uint32_t)(c0 + c), v);
+                if (lr.T) lt.add_block(lr, frag, c, j, fb, features, lane, v);
+                if (j + 16 < ranks) {
+                    tmem_st_frag(trow + (uint32_t)(c0 + c), v);
+                    continue;
                 }
-                if (lr.T) lt.add8(lr, regs, c, nfc, v);
+                for (int q = 0; q < ks - 1; ++q) {
+                    const float* src = xbuf + ((size_t)q * share + c + 2 * (lane & 3)) * kGmM +
+                                       32 * (warp & 3) + (lane >> 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t m = m0 + c0 + c + i;
-                    if (m < prm.M && nf < features) prm.Y[m * features + nf] = __float2half_rn(v[i]);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][i] = __fadd_rn(v[h][i], src[(i & 1) * kGmM + 16 * h + 8 * (i >> 1)]);
+                }
+                uint32_t w[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const __half2 p = __floats2half2_rn(v[h][2 * i], v[h][2 * i + 1]);
+                        w[2 * h + i] = *reinterpret_cast<const uint32_t*>(&p);
+                    }
+                __syncwarp();                            // the last eight have been read
+                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::
+                                 "r"(out_row), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+                __syncwarp();
+                const uint4 u = *reinterpret_cast<const uint4*>(out + 16 * lane);
+                const int64_t m = m0 + c0 + c + (lane >> 2), fo = fb + 8 * (lane & 3);
+                if (m < prm.M) {
+                    __half* dst = prm.Y + m * features + fo;
+                    if (sh.out_vec && fo < features) {
+                        *reinterpret_cast<uint4*>(dst) = u;
+                    } else {
+                        const __half* hs = reinterpret_cast<const __half*>(&u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (fo + i < features) dst[i] = hs[i];
+                    }
                 }
             }
+            LowRankRegs32 regs;
+            regs.init();
             // blocks of eight tokens with several adapters: two tokens for each of
             // the four warps of a quarter (a token's factor loads are a latency each)
             if (lr.T)
 #pragma unroll 1
                 for (int b = 0; b < share; b += 8) {
-                    if (lt.uniform(b)) continue;
+                    if (lt.fast(b)) continue;
 #pragma unroll 1
                     for (int c = b + grp; c < b + 8; c += 4) {
                         float v = tmem_ld1(trow + (uint32_t)(c0 + c));
@@ -647,6 +715,7 @@ cudaError_t launch_gemm_cg(const LinearParams& prm, const LowRankEpi& lr, const 
     const int64_t depth = TRANS ? prm.N : prm.K;
     GemmShape sh;
     sh.tile0 = (int)tile0;
+    sh.out_vec = (TRANS ? prm.K : prm.N) % 8 == 0 && (reinterpret_cast<uintptr_t>(prm.Y) & 15u) == 0;
     sh.bn = plan.bn;
     sh.nmma = plan.bn > 256 ? plan.bn / 2 : plan.bn;
     sh.ks = plan.ks;

@@ -92,6 +92,58 @@ struct LowRankRegs32 {
     __device__ __forceinline__ void init() { a = -1; j0 = 0; }
 };
 
+// x = hi + lo in tf32, rounded by integer additions (the MMA drops the bits below).
+__device__ __forceinline__ void tf32_halves(float x, uint32_t& hi, uint32_t& lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(__fsub_rn(x, __uint_as_float(hi))) + 0x1000u;
+}
+
+__device__ __forceinline__ void mma_tf32_epi(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 ranks (from j) of an adapter's factor at a warp's 32 features as MMA operands:
+// x[h][r][i] = feature 16 h + 8 r + lane / 4, rank j + 4 (lane % 4) + i (the MMA's
+// reduction index is permuted alike in both operands, so that a lane's four ranks
+// are adjacent).
+struct LowRankFrag {
+    float x[2][2][4];
+    int a;
+    __device__ __forceinline__ void init() { a = -1; }
+    __device__ __forceinline__ void load(const LowRankEpi& e, int adapter, int64_t f0,
+                                         int64_t features, int j, int lane) {
+        const int jj = j + 4 * (lane & 3);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int64_t f = f0 + 16 * h + 8 * r + (lane >> 2);
+                const int64_t o = adapter * e.sa + (f < features ? f : features - 1) * e.sf;
+                float* to = x[h][r];
+                if (e.vec) {
+                    uint2 u = make_uint2(0u, 0u);
+                    if (jj < e.rank)                     // (the rank is a multiple of 8)
+                        u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.F) + o + jj));
+                    const float2 p = pair16(u.x, e.dtype), q = pair16(u.y, e.dtype);
+                    to[0] = p.x;
+                    to[1] = p.y;
+                    to[2] = q.x;
+                    to[3] = q.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        to[i] = jj + i < e.rank ? factor_at(e.F, e.dtype, o + (jj + i) * e.sj) : 0.0f;
+                }
+            }
+        a = adapter;
+    }
+};
+
 // A tile's rows of T and its tokens' adapters in shared memory (T stays in global
 // memory where the room is too small for it).
 struct LowRankTile {
@@ -121,20 +173,26 @@ struct LowRankTile {
         }
     }
     // sum of 16 products of the staged token i from rank j (the same for the warp)
+    template <bool STAGED>
     __device__ __forceinline__ float dot16(const LowRankEpi& e, int i, int j,
                                            const float2 (&b)[8]) const {
-        const float4* row = reinterpret_cast<const float4*>((t ? t : rows) + (int64_t)i * e.ld + j);
-        float2 acc = make_float2(0.0f, 0.0f);
+        float4 x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[q] = STAGED ? reinterpret_cast<const float4*>(rows + i * e.ld + j)[q]
+                          : __ldcg(reinterpret_cast<const float4*>(t + (int64_t)i * e.ld + j) + q);
+        float2 acc = make_float2(0.0f, 0.0f), acc2 = acc;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 x = t ? __ldcg(row + q) : row[q];
-            acc = __ffma2_rn(make_float2(x.x, x.y), b[2 * q], acc);
-            acc = __ffma2_rn(make_float2(x.z, x.w), b[2 * q + 1], acc);
+            acc = __ffma2_rn(make_float2(x[q].x, x[q].y), b[2 * q], acc);
+            acc2 = __ffma2_rn(make_float2(x[q].z, x[q].w), b[2 * q + 1], acc2);
         }
+        acc = __fadd2_rn(acc, acc2);
         return __fadd_rn(acc.x, acc.y);
     }
-    // whether staged tokens c .. c + 7 have one adapter (or none) in common
-    __device__ __forceinline__ bool uniform(int c) const {
+    // whether tokens c .. c + 7 are staged and have one adapter (or none) in common
+    __device__ __forceinline__ bool fast(int c) const {
+        if (t != nullptr) return false;
         const int4 a0 = *reinterpret_cast<const int4*>(adapter + c);
         const int4 a1 = *reinterpret_cast<const int4*>(adapter + c + 4);
         const bool same = a0.y == a0.x && a0.z == a0.x && a0.w == a0.x && a1.x == a0.x &&
@@ -150,22 +208,50 @@ struct LowRankTile {
             r.j0 = j;
         }
     }
-    // v[i] += the term of staged token c + i (i < 8) at feature f; uniform(c) holds
-    __device__ __forceinline__ void add8(const LowRankEpi& e, LowRankRegs32& r, int c, int64_t f,
-                                         float (&v)[8]) const {
+    // v[h][e] += ranks j .. j + 15 of the terms of staged tokens c .. c + 7 (fast(c)
+    // holds) at the warp's 32 features from f0, in the layout of an m16n8 MMA: feature
+    // 16 h + lane / 4 + 8 (e / 2), token 2 (lane % 4) + e % 2.  tf32 MMAs: T is split into
+    // two tf32 halves and so are fp32 factors (16-bit ones are exact), which leaves
+    // below 2^-21 of a product; the sum starts at 0 and is added to v with one
+    // rounding.
+    __device__ __forceinline__ void add_block(const LowRankEpi& e, LowRankFrag& r, int c, int j,
+                                              int64_t f0, int64_t features, int lane,
+                                              float (&v)[2][4]) const {
         const int a = adapter[c];
         if (a < 0) return;
-        for (int j = 0; j < e.ld; j += 32) {
-            const bool two = j + 16 < e.ld;
-            load(e, r, a, f, j);
+        if (r.a != a) r.load(e, a, f0, features, j, lane);
+        const float4 x = *reinterpret_cast<const float4*>(rows + (c + (lane >> 2)) * e.ld + j + 4 * (lane & 3));
+        uint32_t hi[4], lo[4];
+        tf32_halves(x.x, hi[0], lo[0]);
+        tf32_halves(x.y, hi[1], lo[1]);
+        tf32_halves(x.z, hi[2], lo[2]);
+        tf32_halves(x.w, hi[3], lo[3]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = __fadd_rn(v[i], dot16(e, c + i, j, r.b[0]));
-                if (two) v[i] = __fadd_rn(v[i], dot16(e, c + i, j + 16, r.b[1]));
+        for (int h = 0; h < 2; ++h) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const float* y0 = r.x[h][0] + 2 * kb;
+                const float* y1 = r.x[h][1] + 2 * kb;
+                uint32_t q0 = __float_as_uint(y0[0]), q1 = __float_as_uint(y1[0]);
+                uint32_t q2 = __float_as_uint(y0[1]), q3 = __float_as_uint(y1[1]);
+                if (e.dtype == 2) {
+                    uint32_t l0, l1, l2, l3;
+                    tf32_halves(y0[0], q0, l0);
+                    tf32_halves(y1[0], q1, l1);
+                    tf32_halves(y0[1], q2, l2);
+                    tf32_halves(y1[1], q3, l3);
+                    mma_tf32_epi(d, l0, l1, l2, l3, hi[2 * kb], hi[2 * kb + 1]);
+                }
+                mma_tf32_epi(d, q0, q1, q2, q3, lo[2 * kb], lo[2 * kb + 1]);
+                mma_tf32_epi(d, q0, q1, q2, q3, hi[2 * kb], hi[2 * kb + 1]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = __fadd_rn(v[h][i], d[i]);
         }
     }
     // the term of staged token c alone
+    template <bool STAGED>
     __device__ __forceinline__ float term(const LowRankEpi& e, LowRankRegs32& r, int c,
                                           int64_t f) const {
         const int a = adapter[c];
@@ -173,10 +259,14 @@ struct LowRankTile {
         if (a >= 0)
             for (int j = 0; j < e.ld; j += 32) {
                 load(e, r, a, f, j);
-                d = __fadd_rn(d, dot16(e, c, j, r.b[0]));
-                if (j + 16 < e.ld) d = __fadd_rn(d, dot16(e, c, j + 16, r.b[1]));
+                d = __fadd_rn(d, dot16<STAGED>(e, c, j, r.b[0]));
+                if (j + 16 < e.ld) d = __fadd_rn(d, dot16<STAGED>(e, c, j + 16, r.b[1]));
             }
         return d;
+    }
+    __device__ __forceinline__ float term(const LowRankEpi& e, LowRankRegs32& r, int c,
+                                          int64_t f) const {
+        return t == nullptr ? term<true>(e, r, c, f) : term<false>(e, r, c, f);
     }
 };
 
