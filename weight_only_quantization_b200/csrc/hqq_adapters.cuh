@@ -13,6 +13,8 @@ struct ShrinkParams {
     const int32_t* index;     // NULL: adapter 0 for every token
     const float* scaling;     // NULL: 1
     float* T;                 // [M, ld]
+    const int32_t* order;     // NULL, or the tokens sorted by adapter ..
+    const int32_t* start;     // .. and where each adapter's begin (start[count]: all)
     int64_t M, K, ldx, sa, sk, sj;
     int ld, rank, count, dtype;
     int beside;               // may run beside the kernel launched before it

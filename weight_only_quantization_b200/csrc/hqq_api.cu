@@ -51,7 +51,7 @@ cudaError_t launch_linear_backward(const LinearParams& prm, const LowRankEpi& lr
                                    int64_t ld, int nbits, cudaStream_t stream);
 cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream);
 cudaError_t launch_order(const int32_t* index, int64_t M, int count, int32_t* order,
-                         int32_t* start, cudaStream_t stream);
+                         int32_t* start, bool beside, cudaStream_t stream);
 cudaError_t launch_factor_grads(FactorGradParams p, cudaStream_t stream);
 cudaError_t launch_pad_rows(const __half* src, int64_t M, int64_t N, int64_t ld, __half* dst,
                             cudaStream_t stream);
@@ -580,6 +580,11 @@ constexpr int kMaxRank = 512, kMaxAdapters = 65535;
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// Whether the small products take the tokens in the adapters' order (a kernel of
+// about 4 us, worth it once tiles of 32 tokens would mix adapters many times over;
+// its work grows with both counts).
+bool in_order(int64_t M, int count) { return M > 256 && count > 1 && count <= 1024; }
+
 // The workspace of an adapter call, as byte offsets: T and P (fp32 [M, ld]), the
 // tokens of each adapter (order, start), and dY with padded rows.
 struct AdapterSpace {
@@ -592,8 +597,9 @@ AdapterSpace adapter_space(int64_t M, int64_t rows, int rank, int count, bool ba
     w.T = 0;
     w.P = mat;
     w.order = w.P + (backward ? mat : 0);
-    w.start = w.order + (backward && rank > 0 ? round_up(M * 4, 256) : 0);
-    w.pad = w.start + (backward && rank > 0 ? round_up(((int64_t)count + 1) * 4, 256) : 0);
+    const bool lists = rank > 0 && (backward || in_order(M, count));
+    w.start = w.order + (lists ? round_up(M * 4, 256) : 0);
+    w.pad = w.start + (lists ? round_up(((int64_t)count + 1) * 4, 256) : 0);
     w.bytes = w.pad + (backward && rows % 8 ? round_up(M * round_up(rows, 8) * 2, 256) : 0);
     return w;
 }
@@ -711,6 +717,14 @@ extern "C" int hqq_linear_adapters(const void* X, int64_t M, const void* packed,
     sh.rank = adapters->rank;
     sh.count = adapters->count;
     sh.dtype = adapters->dtype;
+    if (index && in_order(M, sh.count)) {
+        int32_t* order = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.order);
+        int32_t* start = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.start);
+        if (launch_order(index, M, sh.count, order, start, false, s) != cudaSuccess)
+            return HQQ_ERR_CUDA;
+        sh.order = order;
+        sh.start = start;
+    }
     if (launch_shrink(sh, s) != cudaSuccess) return HQQ_ERR_CUDA;
 
     LowRankEpi lr;
@@ -796,6 +810,15 @@ extern "C" int hqq_linear_adapters_backward(const void* dY, const void* X, int64
         sh.rank = rank;
         sh.count = count;
         sh.dtype = adapters->dtype;
+        int32_t* order = reinterpret_cast<int32_t*>(ws + w.order);
+        int32_t* start = reinterpret_cast<int32_t*>(ws + w.start);
+        const bool sorted = index && in_order(M, count);
+        if (sorted) {
+            if (launch_order(index, M, count, order, start, false, s) != cudaSuccess)
+                return HQQ_ERR_CUDA;
+            sh.order = order;
+            sh.start = start;
+        }
         float* T = reinterpret_cast<float*>(ws + w.T);
         float* P = reinterpret_cast<float*>(ws + w.P);
         if (dB) {                      // T = s X A^T
@@ -824,9 +847,8 @@ extern "C" int hqq_linear_adapters_backward(const void* dY, const void* X, int64
             FactorGradParams fg;
             std::memset(&fg, 0, sizeof fg);
             if (index) {
-                int32_t* order = reinterpret_cast<int32_t*>(ws + w.order);
-                int32_t* start = reinterpret_cast<int32_t*>(ws + w.start);
-                if (launch_order(index, M, count, order, start, s) != cudaSuccess)
+                if (!sorted &&
+                    launch_order(index, M, count, order, start, true, s) != cudaSuccess)
                     return HQQ_ERR_CUDA;
                 fg.order = order;
                 fg.start = start;

@@ -46,6 +46,7 @@ constexpr uint32_t kGmABytes = kGmM * kGmK * 2;
 constexpr uint32_t kGmStageBytes = 196608;       // all stages together (192 KiB)
 constexpr int kGmMaxStages = 8;
 constexpr int kGmTries = 1000;                   // of a wait before it is timed (bounded)
+constexpr int kGmOutRow = 40;                    // floats a staged token (banks apart)
 constexpr int kGmWindow = 256;                   // tokens whose partial sums travel at once
 
 struct GemmShape {
@@ -192,12 +193,20 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const float (&v)[2]
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// One fp32 column of this warp's 32 tensor-memory lanes.
+// One fp32 column of this warp's 32 tensor-memory lanes; the caller waits for the
+// load (tcgen05.wait::ld) before it uses the value.
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     return __uint_as_float(r);
+}
+
+__device__ __forceinline__ void tmem_wait8(float (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7])
+                 :
+                 : "memory");
 }
 
 // 32 codes of one row from a multiple of 32, as loaded: nothing done with a
@@ -324,7 +333,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t bars[3 * kGmMaxStages + 1];
     __shared__ uint32_t tmem_holder;
-    __shared__ __align__(16) uint8_t stage_out[16][512];           // 8 tokens x 32 features a warp
+    __shared__ __align__(16) uint8_t stage_out[16][8 * kGmOutRow * 4];   // 8 tokens x 32 features a warp
     __shared__ int abort_flag;
     const int S = sh.stages, bn = sh.bn, parts = bn / sh.nmma;
     uint8_t* a_st = smem;
@@ -564,6 +573,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
         if (lr.T) lt.stage(lr, m0 + c0, share, prm.M, threadIdx.x, kGmThreads);
         if (ks > 1) cluster_sync_all();
         else __syncthreads();
+        // blocks that mix adapters (or whose T is not staged): tokens in groups
+        const bool mixed = lr.T && __syncthreads_or((int)threadIdx.x < share && lt.mark(threadIdx.x));
+        if (mixed) {
+            lt.group(share, threadIdx.x, kGmThreads);
+            __syncthreads();
+        }
         if (epi) {
             // eight tokens at a time in the layout of an m16n8 MMA, stored through a
             // transposition in shared memory: 64 bytes of a token's row for 4 lanes
@@ -571,18 +586,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
             frag.init();
             uint8_t* out = stage_out[warp - 2];
             const uint32_t out_row = smem_u32(out) + (uint32_t)((lane & 7) * 64 + (lane >> 3) * 16);
+            float* outf = reinterpret_cast<float*>(out);
             const int64_t fb = n0 + 32 * (warp & 3);     // the warp's features
             // (16 ranks a pass: the factor's values stay in registers, the sums go back
             // to tensor memory between passes)
             const int ranks = lr.T ? lr.ld : 16;
 #pragma unroll 1
-            for (int j = 0; j < ranks; j += 16, frag.init())
+            for (int j = 0; j < ranks; j += 16)
 #pragma unroll 1
             for (int c = 8 * grp; c < share; c += 32) {
-                if (lr.T && !lt.fast(c)) continue;       // (below)
+                if (mixed && lt.key[c] != LowRankTile::kFast) continue;   // (below)
                 float v[2][4];
                 tmem_ld_frag(trow + (uint32_t)(c0 + c), v);
-                if (lr.T) lt.add_block(lr, frag, c, j, fb, features, lane, v);
+                if (lr.T && lt.adapter[c] >= 0)
+                    lt.add_block(lr, frag, lt.adapter[c], c + (lane >> 2), j, fb, features, lane, v);
                 if (j + 16 < ranks) {
                     tmem_st_frag(trow + (uint32_t)(c0 + c), v);
                     continue;
@@ -623,22 +640,55 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
                     }
                 }
             }
-            LowRankRegs32 regs;
-            regs.init();
-            // blocks of eight tokens with several adapters: two tokens for each of
-            // the four warps of a quarter (a token's factor loads are a latency each)
-            if (lr.T)
+            // groups of up to eight tokens with one adapter: their columns go through
+            // shared memory to the MMA's layout and back, so that an adapter's factor
+            // is loaded once a group and not once a token
+            if (mixed)
 #pragma unroll 1
-                for (int b = 0; b < share; b += 8) {
-                    if (lt.fast(b)) continue;
-#pragma unroll 1
-                    for (int c = b + grp; c < b + 8; c += 4) {
-                        float v = tmem_ld1(trow + (uint32_t)(c0 + c));
-                        for (int q = 0; q < ks - 1; ++q)
-                            v = __fadd_rn(v, xbuf[((size_t)q * share + c) * kGmM + f]);
-                        v = __fadd_rn(v, lt.term(lr, regs, c, nfc));
+                for (int q = grp; q < *lt.ngroups; q += 4) {
+                    const int first = lt.groups[q] & 0xffff, len = lt.groups[q] >> 16;
+                    const int a = lt.adapter[lt.sorted[first]];
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = tmem_ld1(trow + (uint32_t)(c0 + lt.sorted[first + (i < len ? i : 0)]));
+                    tmem_wait8(v);
+                    if (a >= 0) {
+                        __syncwarp();                    // the last group has been read
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) outf[i * kGmOutRow + lane] = v[i];
+                        __syncwarp();
+                        float w[2][4];
+                        float* at = outf + 2 * (lane & 3) * kGmOutRow + (lane >> 2);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[h][i] = at[(i & 1) * kGmOutRow + 16 * h + 8 * (i >> 1)];
+                        const int tok = (lane >> 2) < len ? lt.sorted[first + (lane >> 2)] : -1;
+                        for (int j = 0; j < lr.ld; j += 32) {    // (two loads in flight)
+                            LowRankFrag other;
+                            if (frag.a != a || frag.j != j) frag.load(lr, a, fb, features, j, lane);
+                            if (j + 16 < lr.ld) other.load(lr, a, fb, features, j + 16, lane);
+                            lt.add_block(lr, frag, a, tok, j, fb, features, lane, w);
+                            if (j + 16 < lr.ld)
+                                lt.add_block(lr, other, a, tok, j + 16, fb, features, lane, w);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) at[(i & 1) * kGmOutRow + 16 * h + 8 * (i >> 1)] = w[h][i];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = outf[i * kGmOutRow + lane];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (i >= len) break;
+                        const int c = lt.sorted[first + i];
+                        for (int r = 0; r < ks - 1; ++r)
+                            v[i] = __fadd_rn(v[i], xbuf[((size_t)r * share + c) * kGmM + f]);
                         const int64_t m = m0 + c0 + c;
-                        if (m < prm.M && nf < features) prm.Y[m * features + nf] = __float2half_rn(v);
+                        if (m < prm.M && nf < features) prm.Y[m * features + nf] = __float2half_rn(v[i]);
                     }
                 }
         }

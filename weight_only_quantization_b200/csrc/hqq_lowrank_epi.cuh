@@ -84,14 +84,6 @@ __device__ __forceinline__ float lowrank_dot16(const float* t, const float2 (&b)
     return __fadd_rn(acc.x, acc.y);
 }
 
-// The factor values of up to 32 ranks that a thread holds from one token to the
-// next: adapter a, ranks from j0.
-struct LowRankRegs32 {
-    float2 b[2][8];
-    int a, j0;
-    __device__ __forceinline__ void init() { a = -1; j0 = 0; }
-};
-
 // x = hi + lo in tf32, rounded by integer additions (the MMA drops the bits below).
 __device__ __forceinline__ void tf32_halves(float x, uint32_t& hi, uint32_t& lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
@@ -113,11 +105,11 @@ __device__ __forceinline__ void mma_tf32_epi(float (&d)[4], uint32_t a0, uint32_
 // are adjacent).
 struct LowRankFrag {
     float x[2][2][4];
-    int a;
-    __device__ __forceinline__ void init() { a = -1; }
+    int a, j;
+    __device__ __forceinline__ void init() { a = -1; j = 0; }
     __device__ __forceinline__ void load(const LowRankEpi& e, int adapter, int64_t f0,
-                                         int64_t features, int j, int lane) {
-        const int jj = j + 4 * (lane & 3);
+                                         int64_t features, int j0, int lane) {
+        const int jj = j0 + 4 * (lane & 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -141,86 +133,103 @@ struct LowRankFrag {
                 }
             }
         a = adapter;
+        j = j0;
     }
 };
 
 // A tile's rows of T and its tokens' adapters in shared memory (T stays in global
-// memory where the room is too small for it).
+// memory where the room is too small for it), and for tiles that mix adapters
+// their tokens in groups of up to eight with one adapter.
 struct LowRankTile {
-    int* adapter;
+    static constexpr int kTokens = 512, kFast = -0x7fffffff - 1;
+    int* adapter;            // [kTokens]
+    int* key;                // [kTokens]: the adapter, or kFast in a block of eight alike
+    int* groups;             // [kTokens]: first place in `sorted` | tokens << 16
+    uint16_t* sorted;        // [kTokens]: tokens by adapter
+    int* ngroups;
     float* rows;
     uint32_t room;           // bytes for rows
     const float* t;          // row 0 of the tokens in global memory, or NULL: staged
     __device__ __forceinline__ void place(uint8_t* mem, uint32_t bytes) {
         adapter = reinterpret_cast<int*>(mem);           // 16-byte aligned
-        rows = reinterpret_cast<float*>(mem + 2048);     // up to 512 tokens
-        room = bytes - 2048u;
+        key = adapter + kTokens;
+        groups = key + kTokens;
+        sorted = reinterpret_cast<uint16_t*>(groups + kTokens);
+        ngroups = reinterpret_cast<int*>(sorted + kTokens);
+        constexpr uint32_t head = kTokens * 14 + 128;
+        rows = reinterpret_cast<float*>(mem + head);
+        room = bytes - head;
         t = nullptr;
     }
     // tokens m .. m + n - 1 (those past M have none), by all `nt` threads of the
-    // CTA; the caller synchronises before add8
+    // CTA; the caller synchronises before using them
     __device__ __forceinline__ void stage(const LowRankEpi& e, int64_t m, int n, int64_t M, int tid,
                                           int nt) {
         for (int i = tid; i < n; i += nt) adapter[i] = m + i < M ? lowrank_adapter(e, m + i) : -1;
+        if (tid == 0) *ngroups = 0;
         const int per = e.ld >> 2;                       // float4s a row
         t = e.T + m * e.ld;
         if ((uint32_t)(n * e.ld) * 4u <= room) {
             const int64_t have = (M - m) * per;
             const int all = n * per < have ? n * per : (int)have;
+#pragma unroll 4
             for (int i = tid; i < all; i += nt)
                 reinterpret_cast<float4*>(rows)[i] = __ldcg(reinterpret_cast<const float4*>(t) + i);
             t = nullptr;
         }
-    }
-    // sum of 16 products of the staged token i from rank j (the same for the warp)
-    template <bool STAGED>
-    __device__ __forceinline__ float dot16(const LowRankEpi& e, int i, int j,
-                                           const float2 (&b)[8]) const {
-        float4 x[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            x[q] = STAGED ? reinterpret_cast<const float4*>(rows + i * e.ld + j)[q]
-                          : __ldcg(reinterpret_cast<const float4*>(t + (int64_t)i * e.ld + j) + q);
-        float2 acc = make_float2(0.0f, 0.0f), acc2 = acc;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            acc = __ffma2_rn(make_float2(x[q].x, x[q].y), b[2 * q], acc);
-            acc2 = __ffma2_rn(make_float2(x[q].z, x[q].w), b[2 * q + 1], acc2);
-        }
-        acc = __fadd2_rn(acc, acc2);
-        return __fadd_rn(acc.x, acc.y);
     }
     // whether tokens c .. c + 7 are staged and have one adapter (or none) in common
     __device__ __forceinline__ bool fast(int c) const {
         if (t != nullptr) return false;
         const int4 a0 = *reinterpret_cast<const int4*>(adapter + c);
         const int4 a1 = *reinterpret_cast<const int4*>(adapter + c + 4);
-        const bool same = a0.y == a0.x && a0.z == a0.x && a0.w == a0.x && a1.x == a0.x &&
-                          a1.y == a0.x && a1.z == a0.x && a1.w == a0.x;
-        return same;
+        return a0.y == a0.x && a0.z == a0.x && a0.w == a0.x && a1.x == a0.x && a1.y == a0.x &&
+               a1.z == a0.x && a1.w == a0.x;
     }
-    __device__ __forceinline__ void load(const LowRankEpi& e, LowRankRegs32& r, int a, int64_t f,
-                                         int j) const {
-        if (r.a != a || r.j0 != j) {
-            lowrank_load16(e, a, f, j, r.b[0]);
-            if (j + 16 < e.ld) lowrank_load16(e, a, f, j + 16, r.b[1]);
-            r.a = a;
-            r.j0 = j;
+    // key[] of token i; whether its block is one to be grouped
+    __device__ __forceinline__ bool mark(int i) {
+        const bool f = fast(i & ~7);
+        key[i] = f ? kFast : adapter[i];
+        return !f;
+    }
+    // Sort those of the n tokens (a multiple of 8) that are not in fast blocks into
+    // groups of one adapter, by all nt threads; the caller synchronises before and
+    // after.  The order of the groups is not fixed, and no result depends on it.
+    __device__ __forceinline__ void group(int n, int tid, int nt) {
+        for (int i = tid; i < n; i += nt) {
+            const int a = key[i];
+            if (a == kFast) continue;
+            int less = 0, before = 0, same = 0;
+#pragma unroll 2
+            for (int j = 0; j < n; j += 4) {
+                const int4 o = *reinterpret_cast<const int4*>(key + j);
+                less += (o.x < a) + (o.y < a) + (o.z < a) + (o.w < a);
+                same += (o.x == a) + (o.y == a) + (o.z == a) + (o.w == a);
+                before += (o.x == a && j < i) + (o.y == a && j + 1 < i) + (o.z == a && j + 2 < i) +
+                          (o.w == a && j + 3 < i);
+            }
+            sorted[less + before] = (uint16_t)i;
+            if ((before & 7) == 0) {
+                const int left = same - before;
+                groups[atomicAdd(ngroups, 1)] = (less + before) | ((left < 8 ? left : 8) << 16);
+            }
         }
     }
-    // v[h][e] += ranks j .. j + 15 of the terms of staged tokens c .. c + 7 (fast(c)
-    // holds) at the warp's 32 features from f0, in the layout of an m16n8 MMA: feature
-    // 16 h + lane / 4 + 8 (e / 2), token 2 (lane % 4) + e % 2.  tf32 MMAs: T is split into
-    // two tf32 halves and so are fp32 factors (16-bit ones are exact), which leaves
-    // below 2^-21 of a product; the sum starts at 0 and is added to v with one
-    // rounding.
-    __device__ __forceinline__ void add_block(const LowRankEpi& e, LowRankFrag& r, int c, int j,
+    // v[h][e] += ranks j .. j + 15 of the terms of eight tokens with adapter a at the
+    // warp's 32 features from f0, in the layout of an m16n8 MMA: feature 16 h + lane / 4 +
+    // 8 (e / 2), token 2 (lane % 4) + e % 2; `tok` is the lane's token lane / 4 (-1:
+    // absent).  tf32 MMAs: T is split into two tf32 halves and so are fp32 factors
+    // (16-bit ones are exact), which leaves below 2^-21 of a product; the sum starts
+    // at 0 and is added to v with one rounding.
+    __device__ __forceinline__ void add_block(const LowRankEpi& e, LowRankFrag& r, int a, int tok, int j,
                                               int64_t f0, int64_t features, int lane,
                                               float (&v)[2][4]) const {
-        const int a = adapter[c];
-        if (a < 0) return;
-        if (r.a != a) r.load(e, a, f0, features, j, lane);
-        const float4 x = *reinterpret_cast<const float4*>(rows + (c + (lane >> 2)) * e.ld + j + 4 * (lane & 3));
+        if (r.a != a || r.j != j) r.load(e, a, f0, features, j, lane);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tok >= 0) {
+            if (t == nullptr) x = *reinterpret_cast<const float4*>(rows + tok * e.ld + j + 4 * (lane & 3));
+            else x = __ldcg(reinterpret_cast<const float4*>(t + (int64_t)tok * e.ld + j + 4 * (lane & 3)));
+        }
         uint32_t hi[4], lo[4];
         tf32_halves(x.x, hi[0], lo[0]);
         tf32_halves(x.y, hi[1], lo[1]);
@@ -249,24 +258,6 @@ struct LowRankTile {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[h][i] = __fadd_rn(v[h][i], d[i]);
         }
-    }
-    // the term of staged token c alone
-    template <bool STAGED>
-    __device__ __forceinline__ float term(const LowRankEpi& e, LowRankRegs32& r, int c,
-                                          int64_t f) const {
-        const int a = adapter[c];
-        float d = 0.0f;
-        if (a >= 0)
-            for (int j = 0; j < e.ld; j += 32) {
-                load(e, r, a, f, j);
-                d = __fadd_rn(d, dot16<STAGED>(e, c, j, r.b[0]));
-                if (j + 16 < e.ld) d = __fadd_rn(d, dot16<STAGED>(e, c, j + 16, r.b[1]));
-            }
-        return d;
-    }
-    __device__ __forceinline__ float term(const LowRankEpi& e, LowRankRegs32& r, int c,
-                                          int64_t f) const {
-        return t == nullptr ? term<true>(e, r, c, f) : term<false>(e, r, c, f);
     }
 };
 
