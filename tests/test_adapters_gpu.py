@@ -555,3 +555,34 @@ def test_large_tiles_exact(hqq, rows, cols, M, nbits):
     dA, dB = torch.einsum("maj,mk->ajk", P, x), torch.einsum("maj,mn->anj", T, y)
     assert max(float(dA.abs().max()), float(dB.abs().max())) < 2 ** 24
     assert torch.equal(got[1], dA.float()) and torch.equal(got[2], dB.float())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rank", [40, 104, 512])
+@pytest.mark.parametrize("kind", ["one", "runs", "mixed"])
+def test_high_ranks_on_many_tokens(hqq, dtype, rank, kind):
+    """Several passes of 16 ranks over the sums, in tiles of one adapter and of
+    several; 512 ranks do not fit beside the tile in shared memory."""
+    rows, cols, M, count = 264, 528, 300, 1 if kind == "one" else 3
+    q, W = matrix(hqq, rows, cols, 4, 16, seed=rank)
+    ad = adapters(hqq, count, rank, rows, cols, TYPES[dtype], seed=rank)
+    check_both(hqq, q, W, ad, M, indices(M, count, kind, rank), seed=rank)
+
+
+@pytest.mark.parametrize("M", [12, 70, 300, 700])
+@pytest.mark.parametrize("rank", [16, 40])
+def test_a_token_does_not_depend_on_the_others_adapters(hqq, M, rank):
+    """The same bits for a token whether its neighbours have its adapter, others
+    or none."""
+    rows, cols, count = 264, 512, 4
+    q, _ = matrix(hqq, rows, cols, 3, 64, seed=M)
+    ad = adapters(hqq, count, rank, rows, cols, torch.float16, seed=rank)
+    X, dY = tokens(M, cols, 6).cuda(), tokens(M, rows, 7).cuda()
+    same = torch.full((M,), 2, dtype=torch.int32, device="cuda")
+    other = indices(M, count, "mixed", 3).cuda()
+    Y = hqq.hqq_linear_adapters(X, q, ad, same)
+    Z = hqq.hqq_linear_adapters(X, q, ad, other)
+    dX = hqq.hqq_linear_adapters_backward(dY, None, q, ad, same, need_factors=False)[0]
+    dZ = hqq.hqq_linear_adapters_backward(dY, None, q, ad, other, need_factors=False)[0]
+    at = other == 2
+    assert bool(at.any()) and torch.equal(Y[at], Z[at]) and torch.equal(dX[at], dZ[at])

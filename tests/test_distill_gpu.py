@@ -6,11 +6,12 @@ and a = |z - max| log2(e) / t:
 - an exponential 2^a is formed from a difference, a product and a rounded
   constant (3 u of a each) and ex2.approx (2^-22): relative error
   (3 ln2 a + 4) u <= (2.1 a + 4) u;
-- the row's sum adds at most 64 values a thread and round, then 5 + 15 + 7
-  pairwise joins of up to 4 roundings: at most D = 64 rounds + 110 roundings
-  (rounds = 1 while the row fits the registers of its CTAs), so the sum's
-  relative error is es = (2.1 R + 4 + D) u, with R the largest a whose term
-  matters (terms beyond a = 40 are below 2^-40 of the sum);
+- a thread's sum takes 16 pair additions and 4 more per four packs of 16 bytes, at
+  most 4 times for a 64 KiB share of the row (12 for the longest kept share),
+  then 5 + 3 + 3 joining steps of 2: at most 102 roundings, 262 for rows of more
+  than 131072 values; D = 174, and 64 per 16384 values + 110 above, cover
+  both, so the sum's relative error is es = (2.1 R + 4 + D) u, with R the
+  largest a whose term matters (terms beyond a = 40 are below 2^-40 of the sum);
 - p_k likewise: ep = (2.1 Rt + 8 + K / 32 + 8) u + 4 u (|t_k| / t + |L|), the
   second part the rounded difference of two logits;
 - loss terms: p_k (log p_k - log q_k), each logarithm a difference of values
@@ -21,7 +22,6 @@ and a = |z - max| log2(e) / t:
 """
 import math
 
-import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu

@@ -21,9 +21,22 @@
 // memory, added in rank order).
 // What the choice of bn, ks and CG weighs is at plan_gemm below.
 //
-// Warps: 0 TMA, 1 MMA and tensor memory, 2..17 producers; all join the epilogue,
-// where the low-rank term is added in fp32 from factors in registers and T in
-// shared memory.  Every mbarrier wait is bounded (hqq_tcgen05.cuh); after one has
+// Warps: 0 TMA, 1 MMA and tensor memory, 2..17 producers, which also run the
+// epilogue: the sums are read in the layout of an m16n8 MMA, the low-rank term is
+// added to them 16 ranks a pass (factors in registers, T in shared memory) and the
+// rounded outputs go through shared memory into rows of 64 bytes.  Tokens of several
+// adapters in one block of eight are grouped by adapter first.  (On CUDA cores every
+// product needs its own broadcast of T, four cycles of shared memory per 16 bytes:
+// 28672 x 8192, 2048 tokens, rank 64: 1640 us against 1176.)
+//
+// What bounds it: at 512 tokens a tile 128 reduction steps take 0.97 us each where
+// the MMAs need 0.74 (8192 x 8192 at 3 bits, 2048 tokens: 262 us, 1050 TFLOP/s); the
+// rest is the pair's handshake and the producers' loads and decode (timing-only
+// copies: 0.81 us without the code loads).  At up to 256 tokens a step takes 0.60 us
+// whatever bn: producers and handshake.  What these were measured against: arrivals
+// at cluster scope by every producer warp 1.66 us a step (they wait for the code
+// loads in flight), waits as calls that read the clock 0.15 us more, 16 codes a
+// thread instead of 64 1.05 us.  Every mbarrier wait is bounded (hqq_tcgen05.cuh); after one has
 // run out the CTA still drains its own copies and MMAs, and the result is
 // unspecified.
 #pragma once

@@ -3,9 +3,10 @@
 //   sum_j T[m, j] * F[a, f, j],
 // T [M, ld] fp32 already scaled (hqq_adapters.cu), ld = the rank rounded up to 16
 // with zeros behind it; F is the adapters' second factor (B for the layer, A for
-// its input gradient) in fp16, bf16 or fp32, addressed by strides.  The sum runs
-// over j in fp32 fused multiply-adds.  A token without an adapter is skipped
-// (its row of T is never read).
+// its input gradient) in fp16, bf16 or fp32, addressed by strides.  The few-token
+// kernels sum over j in fp32 fused multiply-adds, the tensor-memory kernel in tf32
+// MMAs with T (and fp32 factors) split into two halves.  A token without an adapter
+// has no term (its row of T may hold anything).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -161,15 +162,21 @@ struct LowRankTile {
         room = bytes - head;
         t = nullptr;
     }
-    // tokens m .. m + n - 1 (those past M have none), by all `nt` threads of the
-    // CTA; the caller synchronises before using them
+    // tokens m .. m + n - 1, by all `nt` threads of the CTA; the caller synchronises
+    // before using them.  Those past M, whose results are not stored, count as the
+    // last token's neighbours (their staged rows hold anything); where T is not
+    // staged they have no adapter, so that no row past M is read.
     __device__ __forceinline__ void stage(const LowRankEpi& e, int64_t m, int n, int64_t M, int tid,
                                           int nt) {
-        for (int i = tid; i < n; i += nt) adapter[i] = m + i < M ? lowrank_adapter(e, m + i) : -1;
+        const bool fits = (uint32_t)(n * e.ld) * 4u <= room;
+        for (int i = tid; i < n; i += nt) {
+            const int64_t at = m + i < M ? m + i : fits && m < M ? M - 1 : -1;
+            adapter[i] = at >= 0 ? lowrank_adapter(e, at) : -1;
+        }
         if (tid == 0) *ngroups = 0;
         const int per = e.ld >> 2;                       // float4s a row
         t = e.T + m * e.ld;
-        if ((uint32_t)(n * e.ld) * 4u <= room) {
+        if (fits) {
             const int64_t have = (M - m) * per;
             const int all = n * per < have ? n * per : (int)have;
 #pragma unroll 4
