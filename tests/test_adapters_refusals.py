@@ -104,3 +104,25 @@ def test_workspace_bytes(lib):
                 (4, 64, 128, 0, 2, 0), (4, 64, 128, 513, 2, 0), (4, 64, 128, 8, 0, 0),
                 (4, 64, 128, 8, 65536, 1), (4, 64, 128, -1, 1, 1)):
         assert f(*bad) == -1
+
+
+def test_binding_refusals(lib):
+    """No CPU path, and shapes and types are checked before the library is called."""
+    torch = pytest.importorskip("torch")
+    q = lib.QuantizedMatrix(torch.zeros(64 * 128 // 2, dtype=torch.uint8),
+                            torch.zeros(64, 2, dtype=torch.float16),
+                            torch.zeros(64, 2, dtype=torch.float16), 64, 128, 4, 64)
+    ad = lib.Adapters(torch.zeros(2, 8, 128).half(), torch.zeros(2, 64, 8).half())
+    X, dY = torch.zeros(3, 128).half(), torch.zeros(3, 64).half()
+    index = torch.zeros(3, dtype=torch.int32)
+    for bad in (dict(), dict(index=index), dict(index=index.long())):
+        with pytest.raises(ValueError):
+            lib.hqq_linear_adapters(X, q, ad, **bad)
+        with pytest.raises(ValueError):
+            lib.hqq_linear_adapters_backward(dY, X, q, ad, **bad)
+    with pytest.raises(ValueError):
+        lib.hqq_linear_adapters(X.float(), q, ad)
+    with pytest.raises(ValueError):
+        lib.hqq_linear_adapters_backward(dY, None, q, ad)
+    with pytest.raises(ValueError):
+        lib.hqq_linear_adapters_backward(dY, None, q, index=index)

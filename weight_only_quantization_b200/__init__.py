@@ -445,23 +445,27 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _run_on(t, stream, others, fn, *args):
-    """fn(*args, stream) with t's device current; every other tensor given must
-    live there, and so must the stream (None: the device's current one)."""
+def _need(t, name, dev):
+    """A contiguous tensor on CUDA device dev (None passes)."""
+    if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
+
+
+def _run_on(dev, stream, fn, *args):
+    """fn(*args, stream) with CUDA device dev current, on the given stream of it (None:
+    its current one)."""
     import torch
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError(f"all tensors must be on {t.device}")
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    elif stream.device != t.device:
-        raise ValueError(f"stream must be on {t.device}")
+    elif stream.device.index != dev:
+        raise ValueError(f"stream must be on cuda:{dev}")
     if torch.cuda.current_device() == dev:
-        _check(fn(*args, stream.cuda_stream))
+        st = fn(*args, stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream))
+            st = fn(*args, stream.cuda_stream)
+    if st != 0:
+        raise HQQError(st)
 
 
 def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher_lse=None,
@@ -480,28 +484,31 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
         raise ValueError("logits must be a CUDA [tokens, vocab] tensor with adjacent columns")
     dt = _dtype_code(logits.dtype, "logits")
     tokens, vocab = logits.shape
+    dev = logits.get_device()
     if top_logits.dim() != 2 or top_logits.shape != top_index.shape or \
             top_logits.shape[0] != tokens:
         raise ValueError("top_logits and top_index must be [tokens, top_k] tensors")
     if top_index.dtype not in (torch.int32, torch.int64):
         raise ValueError("top_index must be int32 or int64")
-    for t, nm in ((top_logits, "top_logits"), (top_index, "top_index"),
-                  (teacher_lse, "teacher_lse"), (weight, "weight"), (loss, "loss"), (lse, "lse")):
-        _check_tensor(t, nm)
+    _need(top_logits, "top_logits", dev)
+    _need(top_index, "top_index", dev)
     for t, nm in ((teacher_lse, "teacher_lse"), (weight, "weight"), (loss, "loss"), (lse, "lse")):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != tokens):
-            raise ValueError(f"{nm} must be a float32 [tokens] tensor")
+        if t is not None:
+            _need(t, nm, dev)
+            if t.dtype != torch.float32 or t.numel() != tokens:
+                raise ValueError(f"{nm} must be a float32 [tokens] tensor")
     if grad is True:
-        grad = torch.empty((tokens, vocab), dtype=logits.dtype, device=logits.device)
+        grad = torch.empty_like(logits) if logits.is_contiguous() else \
+            torch.empty((tokens, vocab), dtype=logits.dtype, device=logits.device)
     elif grad is False:
         grad = None
     elif grad.dtype != logits.dtype or grad.shape != logits.shape or \
-            (vocab > 1 and grad.stride(1) != 1):
+            grad.get_device() != dev or (vocab > 1 and grad.stride(1) != 1):
         raise ValueError("grad must be like logits")
     if loss is None:
-        loss = torch.empty(tokens, dtype=torch.float32, device=logits.device)
+        loss = logits.new_empty(tokens, dtype=torch.float32)
     if lse is None:
-        lse = torch.empty(tokens, dtype=torch.float32, device=logits.device)
+        lse = torch.empty_like(loss)
     # (a single row may report any stride)
     rows = grows = vocab
     if tokens > 1:
@@ -509,11 +516,10 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
         grows = vocab if grad is None else grad.stride(0)
         if rows < vocab or grows < vocab:
             raise ValueError("rows of logits and grad must not overlap")
-    _run_on(logits, stream, (top_logits, top_index, teacher_lse, weight, grad, loss, lse),
-            _lib.hqq_distill, logits.data_ptr(), rows, dt, tokens, vocab, top_logits.data_ptr(),
-            _dtype_code(top_logits.dtype, "top_logits"), top_index.data_ptr(),
-            top_index.element_size(), top_logits.shape[1], temperature, _addr(teacher_lse),
-            _addr(weight), loss.data_ptr(), lse.data_ptr(), _addr(grad), grows)
+    _run_on(dev, stream, _lib.hqq_distill, logits.data_ptr(), rows, dt, tokens, vocab,
+            top_logits.data_ptr(), _dtype_code(top_logits.dtype, "top_logits"),
+            top_index.data_ptr(), top_index.element_size(), top_logits.shape[1], temperature,
+            _addr(teacher_lse), _addr(weight), loss.data_ptr(), lse.data_ptr(), _addr(grad), grows)
     return loss, lse, grad
 
 
@@ -525,7 +531,7 @@ class Adapters:
     B: "torch.Tensor"          # the same type  [count, rows, rank] (or [rows, rank])
     scaling: "torch.Tensor | None" = None   # fp32 [count]; None: 1
 
-    def _c(self, rows: int, cols: int):
+    def _c(self, rows: int, cols: int, dev: int):
         A, B, scaling = self.A, self.B, self.scaling
         if A.dim() == 2:
             A = A.unsqueeze(0)
@@ -547,11 +553,11 @@ class Adapters:
                     raise ValueError(f"the adapters of {nm} must not overlap")
             if count > 1:
                 a_stride, b_stride = A.stride(0), B.stride(0)
-        if not (A.is_cuda and B.is_cuda):
-            raise ValueError("adapters must be CUDA tensors")
+        if A.get_device() != dev or B.get_device() != dev:
+            raise ValueError(f"adapters must be on cuda:{dev}")
         s = None
         if scaling is not None:
-            _check_tensor(scaling, "scaling")
+            _need(scaling, "scaling", dev)
             if _dtype_code(scaling.dtype, "scaling") != 2 or scaling.numel() != count:
                 raise ValueError("scaling must be a float32 [count] tensor")
             s = scaling.data_ptr()
@@ -566,28 +572,30 @@ def _adapter_call(fn, lead, tail, x, q, adapters, index, zero_q, scale_q, M, bac
     import torch
     if index is not None and (index.dtype != torch.int32 or index.numel() != M):
         raise ValueError("index must be an int32 [M] tensor")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
     zero = q.zero if zero_q is None else None
     scale = q.scale if scale_q is None else None
     for t, nm in ((q.packed, "packed"), (index, "index"), (workspace, "workspace"),
                   (zero, "zero"), (scale, "scale"), *tensors):
-        _check_tensor(t, nm)
-    used = [q.packed, index, workspace, zero, scale, *(t for t, _ in tensors)]
+        _need(t, nm, dev)
     ca, rank, count = None, 0, 0
     if adapters is not None:
-        ca = adapters._c(q.rows, q.cols)
+        ca = adapters._c(q.rows, q.cols, dev)
         rank, count = ca.rank, ca.count
-        used += (adapters.A, adapters.B, adapters.scaling)
     for m in (zero_q, scale_q):
         if m is not None:
-            used += (m.codes, m.scale, m.zero)
+            for t in (m.codes, m.scale, m.zero):
+                _need(t, "8-bit meta data", dev)
     need = _lib.hqq_linear_adapters_workspace_bytes(M, q.rows, q.cols, rank, count, backward)
     if need < 0:
         raise HQQError(2 if ca is None or (0 < rank <= 512 and 0 < count <= 65535) else 4)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     byref = ctypes.byref
-    _run_on(x, stream, used, fn, *lead, M, q.packed.data_ptr(), _addr(scale), _addr(zero),
+    _run_on(dev, stream, fn, *lead, M, q.packed.data_ptr(), _addr(scale), _addr(zero),
             None if zero_q is None else byref(zero_q._c()),
             None if scale_q is None else byref(scale_q._c()), q.rows, q.cols, q.nbits, q.group,
             None if ca is None else byref(ca), _addr(index), *tail, _addr(workspace), nbytes)
@@ -605,7 +613,7 @@ def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, o
         raise ValueError("X must be a float16 [M, cols] tensor")
     M = X.shape[0]
     if out is None:
-        out = torch.empty((M, q.rows), dtype=torch.float16, device=X.device)
+        out = X.new_empty((M, q.rows))
     elif out.dtype != torch.float16 or out.numel() != M * q.rows:
         raise ValueError("out must be a float16 [M, rows] tensor")
     _adapter_call(_lib.hqq_linear_adapters, (X.data_ptr(),), (out.data_ptr(), _addr(status)), X, q,
@@ -637,16 +645,16 @@ def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters |
     if not need_dX:
         dX = None
     elif dX is None:
-        dX = torch.empty((M, q.cols), dtype=torch.float16, device=dY.device)
+        dX = dY.new_empty((M, q.cols))
     elif dX.dtype != torch.float16 or dX.numel() != M * q.cols:
         raise ValueError("dX must be a float16 [M, cols] tensor")
     if need_factors:
         count = adapters.A.shape[0] if adapters.A.dim() == 3 else 1
         rank = adapters.A.shape[-2]
         if dA is None:
-            dA = torch.empty((count, rank, q.cols), dtype=torch.float32, device=dY.device)
+            dA = dY.new_empty((count, rank, q.cols), dtype=torch.float32)
         if dB is None:
-            dB = torch.empty((count, q.rows, rank), dtype=torch.float32, device=dY.device)
+            dB = dY.new_empty((count, q.rows, rank), dtype=torch.float32)
         if dA.dtype != torch.float32 or dA.numel() != count * rank * q.cols or \
                 dB.dtype != torch.float32 or dB.numel() != count * rank * q.rows:
             raise ValueError("dA and dB must be float32 [count, rank, cols] and "
