@@ -834,7 +834,7 @@ cudaError_t launch_gemm_n(const LinearParams& prm, const LowRankEpi& lr, const v
     const GemmPlan plan = plan_gemm(prm.M, features, depth, sms);
     // A nearly empty last round is a launch of its own, with the tiles that suit
     // what is left: the gate matrix at 2048 tokens is 448 pair tiles, 6 rounds of 74
-    // and 4 tiles over (a seventh round of 142 us; on their own about 30).
+    // and 4 tiles over (a seventh round of 142 us; on their own about 40).
     const int64_t whole = plan.rows * plan.cg;
     if (whole > 0 && whole < tiles) {
         const GemmPlan rest = plan_gemm(prm.M, features - whole * kGmM, depth, sms);
