@@ -40,9 +40,11 @@ typedef enum hqq_status {
     HQQ_ERR_NULL = 1,        /* a required pointer is NULL                       */
     HQQ_ERR_SHAPE = 2,       /* rows/cols negative, cols % group != 0, too large */
     HQQ_ERR_UNSUPPORTED = 3, /* nbits not in {1,2,3,4,8}, group not in {16..256,
-                                2^k}, meta group not 0 or 2^k                    */
+                                2^k}, meta group not 0 or 2^k, unknown dtype     */
     HQQ_ERR_PARAM = 4,       /* p not in (0,1], beta/kappa not > 0 and finite,
-                                iters not in [0,255]                             */
+                                iters not in [0,255]; adapter rank or count out
+                                of range, workspace too small; temperature not
+                                > 0 and finite                                   */
     HQQ_ERR_ALIGN = 5,       /* W / W_out / X not 16-byte aligned; packed not
                                 4-byte (8-byte at 8 bits); zero_f32 or err_out
                                 not 4-byte; scale/zero not 2-byte                */

@@ -148,9 +148,9 @@ extern "C" const char* hqq_status_string(int status) {
     switch (status) {
         case HQQ_OK: return "HQQ_OK";
         case HQQ_ERR_NULL: return "HQQ_ERR_NULL: a required pointer is NULL";
-        case HQQ_ERR_SHAPE: return "HQQ_ERR_SHAPE: bad rows/cols or cols not a multiple of group";
-        case HQQ_ERR_UNSUPPORTED: return "HQQ_ERR_UNSUPPORTED: nbits must be 1/2/3/4/8, group 16..256 (power of two), meta group 0 or a power of two up to 2^30";
-        case HQQ_ERR_PARAM: return "HQQ_ERR_PARAM: need 0<p<=1, beta>0, kappa>0 (finite), 0<=iters<=255";
+        case HQQ_ERR_SHAPE: return "HQQ_ERR_SHAPE: bad rows/cols/tokens/vocab, a stride below its row, or cols not a multiple of group";
+        case HQQ_ERR_UNSUPPORTED: return "HQQ_ERR_UNSUPPORTED: nbits must be 1/2/3/4/8, group 16..256 (power of two), meta group 0 or a power of two up to 2^30, dtype fp16/bf16/fp32, index int32/int64";
+        case HQQ_ERR_PARAM: return "HQQ_ERR_PARAM: need 0<p<=1, beta>0, kappa>0 (finite), 0<=iters<=255; adapters: rank 1..512, count 1..65535, one form of scale and zero, the whole workspace; temperature > 0 (finite)";
         case HQQ_ERR_ALIGN: return "HQQ_ERR_ALIGN: W/W_out/X/meta x/meta out need 16-byte, meta codes and 8-bit packed 8-byte, packed/zero_f32 4-byte, scale/zero 2-byte alignment";
         case HQQ_ERR_CUDA: return "HQQ_ERR_CUDA: kernel launch failed (see cudaGetLastError)";
         case HQQ_ERR_SCRATCH: return "HQQ_ERR_SCRATCH: the problem needs more scratch than the fixed array of hqq_lowrank_noalloc holds (hqq_lowrank_noalloc_max_bytes)";
