@@ -449,6 +449,9 @@ int64_t hqq_linear_adapters_workspace_bytes(int64_t M, int64_t rows, int64_t col
  *  - index NULL: every token has adapter 0.
  *  - Tokens need no order; a token's result does not depend on the other tokens'
  *    values or adapters (beyond the summation order of its token count).
+ *  - Values that are not finite stay so: a NaN in a sum gives NaN; an infinity
+ *    gives an infinity or NaN (fp32 values enter products as two halves).  The
+ *    same holds for the gradients below.
  *   X, M, packed, scale, zero, rows, cols, nbits, group, Y, status  as for
  *            hqq_linear; zero_q / scale_q (HOST pointers or NULL) replace zero /
  *            scale by their 8-bit forms as in hqq_linear_meta: exactly one of

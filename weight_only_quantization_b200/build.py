@@ -20,7 +20,8 @@ SOURCES = ["hqq_api.cu", "hqq_quantize.cu", "hqq_quantize_half.cu", "hqq_dequant
            "hqq_distill.cu", "hqq_adapters.cu", "hqq_linear_adapters.cu",
            "hqq_linear_backward.cu", "hqq_decode_adapters.cu"]
 HEADERS = ["hqq_common.cuh", "hqq_params.cuh", "hqq_unpack.cuh", "hqq_quantize.cuh",
-           "hqq_tcgen05.cuh", "hqq_gemm.cuh", "hqq_decode.cuh", "hqq_lowrank_epi.cuh", "hqq_adapters.cuh"]
+           "hqq_tcgen05.cuh", "hqq_gemm.cuh", "hqq_decode.cuh", "hqq_lowrank_epi.cuh", "hqq_adapters.cuh",
+           "hqq_tf32.cuh"]
 LIB = os.path.join(PKG, "libhqq.so")
 
 COMPILE_FLAGS = [

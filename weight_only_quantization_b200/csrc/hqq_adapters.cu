@@ -35,9 +35,9 @@
 // integer rounding and the copies' addresses hoisted), bound by instruction issue and
 // the tf32 MMAs, not by its 67 MB.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
 
 #include "hqq_adapters.cuh"
+#include "hqq_tf32.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -59,23 +59,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// x = hi + lo with both in tf32, rounded to nearest by integer additions (the MMA
-// drops the bits below lo's): the rest is below 2^-22 |x|.  The conversion
-// instruction measured slower.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    lo = __float_as_uint(__fsub_rn(x, __uint_as_float(hi))) + 0x1000u;
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -91,11 +74,11 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// How a factor's values reach the B operand.
 // A kernel launched beside the one before it does not end before that one: what
 // waits for its end may rely on both.
 __device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// How a factor's values reach the B operand.
 enum FactorForm {
     kKPairs,     // fp16, the reduction index contiguous: one 16-byte load a lane
     kJPairs,     // fp16, the rank contiguous: 8x8 blocks transposed in registers
@@ -105,14 +88,6 @@ enum FactorForm {
     kJF32,
     kAnyType     // any type and strides, tf32 MMAs
 };
-
-__device__ __forceinline__ float factor_val(const void* F, int dtype, int64_t o) {
-    switch (dtype) {
-        case 0: return __half2float(__ldg(static_cast<const __half*>(F) + o));
-        case 1: return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(F) + o));
-        default: return __ldg(static_cast<const float*>(F) + o);
-    }
-}
 
 // Grid: x = ((tile * slots) + slot) * csize + cluster rank, y = chunks of 8 NT
 // ranks.
@@ -288,7 +263,7 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             v[n][i] = j < p.rank && kk + i < p.K
-                                          ? factor_val(p.F, p.dtype, fo + j * p.sj + (kk + i) * p.sk)
+                                          ? factor_at(p.F, p.dtype, fo + j * p.sj + (kk + i) * p.sk)
                                           : 0.0f;
                     }
                 }

@@ -8,9 +8,8 @@
 // MMAs with T (and fp32 factors) split into two halves.  A token without an adapter
 // has no term (its row of T may hold anything).
 #pragma once
-#include <cuda_bf16.h>
-
 #include "hqq_params.cuh"
+#include "hqq_tf32.cuh"
 
 namespace hqq {
 
@@ -32,15 +31,6 @@ struct LowRankEpi {
 __device__ __forceinline__ int lowrank_adapter(const LowRankEpi& e, int64_t m) {
     const int a = e.index ? __ldg(e.index + m) : 0;
     return (unsigned)a < (unsigned)e.count ? a : -1;
-}
-
-// A factor's value at element offset o.
-__device__ __forceinline__ float factor_at(const void* F, int dtype, int64_t o) {
-    switch (dtype) {
-        case 0: return __half2float(__ldg(static_cast<const __half*>(F) + o));
-        case 1: return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(F) + o));
-        default: return __ldg(static_cast<const float*>(F) + o);
-    }
 }
 
 __device__ __forceinline__ float2 pair16(uint32_t u, int dtype) {
@@ -83,21 +73,6 @@ __device__ __forceinline__ float lowrank_dot16(const float* t, const float2 (&b)
         acc = __ffma2_rn(make_float2(q.z, q.w), b[2 * i + 1], acc);
     }
     return __fadd_rn(acc.x, acc.y);
-}
-
-// x = hi + lo in tf32, rounded by integer additions (the MMA drops the bits below).
-__device__ __forceinline__ void tf32_halves(float x, uint32_t& hi, uint32_t& lo) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    lo = __float_as_uint(__fsub_rn(x, __uint_as_float(hi))) + 0x1000u;
-}
-
-__device__ __forceinline__ void mma_tf32_epi(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 16 ranks (from j) of an adapter's factor at a warp's 32 features as MMA operands:
@@ -238,10 +213,10 @@ struct LowRankTile {
             else x = __ldcg(reinterpret_cast<const float4*>(t + (int64_t)tok * e.ld + j + 4 * (lane & 3)));
         }
         uint32_t hi[4], lo[4];
-        tf32_halves(x.x, hi[0], lo[0]);
-        tf32_halves(x.y, hi[1], lo[1]);
-        tf32_halves(x.z, hi[2], lo[2]);
-        tf32_halves(x.w, hi[3], lo[3]);
+        split_tf32(x.x, hi[0], lo[0]);
+        split_tf32(x.y, hi[1], lo[1]);
+        split_tf32(x.z, hi[2], lo[2]);
+        split_tf32(x.w, hi[3], lo[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -253,14 +228,14 @@ struct LowRankTile {
                 uint32_t q2 = __float_as_uint(y0[1]), q3 = __float_as_uint(y1[1]);
                 if (e.dtype == 2) {
                     uint32_t l0, l1, l2, l3;
-                    tf32_halves(y0[0], q0, l0);
-                    tf32_halves(y1[0], q1, l1);
-                    tf32_halves(y0[1], q2, l2);
-                    tf32_halves(y1[1], q3, l3);
-                    mma_tf32_epi(d, l0, l1, l2, l3, hi[2 * kb], hi[2 * kb + 1]);
+                    split_tf32(y0[0], q0, l0);
+                    split_tf32(y1[0], q1, l1);
+                    split_tf32(y0[1], q2, l2);
+                    split_tf32(y1[1], q3, l3);
+                    mma_tf32(d, l0, l1, l2, l3, hi[2 * kb], hi[2 * kb + 1]);
                 }
-                mma_tf32_epi(d, q0, q1, q2, q3, lo[2 * kb], lo[2 * kb + 1]);
-                mma_tf32_epi(d, q0, q1, q2, q3, hi[2 * kb], hi[2 * kb + 1]);
+                mma_tf32(d, q0, q1, q2, q3, lo[2 * kb], lo[2 * kb + 1]);
+                mma_tf32(d, q0, q1, q2, q3, hi[2 * kb], hi[2 * kb + 1]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[h][i] = __fadd_rn(v[h][i], d[i]);
