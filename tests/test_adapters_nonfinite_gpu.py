@@ -143,3 +143,27 @@ def test_factor_near_the_largest_value(hqq):
     assert float(dB[0, 5, 3]) == float(big) * 2.0 ** -10
     dB[0, 5, 3] = 0.0
     assert bool((dB == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [4, 70])
+@pytest.mark.parametrize("rank", [1, 5, 8, 13, 16, 40])
+def test_an_infinity_among_positive_values(hqq, dtype, M, rank):
+    """With every weight and factor positive an infinite X gives a row of infinities,
+    and an infinite dY one of dX, whether or not the rank fills the rows of 16 that T
+    and P are kept in."""
+    rows, cols, count = 200, 320, 3
+    q, _ = matrix(hqq, rows, cols, 4, 64, seed=rank)
+    q.zero.fill_(-1.0)
+    ad = adapters(hqq, count, rank, rows, cols, TYPES[dtype], seed=rank)
+    for F in (ad.A, ad.B):
+        F.abs_().add_(0.5)
+    index = torch.arange(M, dtype=torch.int32) % count
+    X, dY = tokens(M, cols, 6), tokens(M, rows, 7, 0.25)
+    clean = run(hqq, q, ad, index.cuda(), X.cuda(), dY.cuda())
+    X[1, 100] = dY[1, 33] = math.inf
+    got = run(hqq, q, ad, index.cuda(), X.cuda(), dY.cuda())
+    for g, c in zip(got[:2], clean[:2]):
+        assert bool((g[1] == math.inf).all())
+        g[1] = c[1] = 0.0
+        assert torch.equal(g, c)

@@ -357,7 +357,8 @@ shrink_kernel(const __grid_constant__ ShrinkParams p, int csize, int slots) {
                 const int e = u * kShThreads + tid;
                 const int row = e / RC, j = j0 + e % RC;
                 if ((TE % kShThreads == 0 || e < TE) && (same >> row & 1u) && j < p.ld)
-                    p.T[(int64_t)toks[row] * p.ld + j] = __fmul_rn(v[u], s);
+                    // (behind the rank: an infinite X times 0 would be NaN)
+                    p.T[(int64_t)toks[row] * p.ld + j] = j < p.rank ? __fmul_rn(v[u], s) : 0.0f;
             }
         }
         __syncthreads();                                 // red is written again
