@@ -445,8 +445,12 @@ cudaError_t launch_ds(const DistillParams& p, int csize, int share_packs, cudaSt
     auto kern = distill_kernel<T, CACHED>;
     const size_t smem = (CACHED ? (size_t)share_packs * 16 : 0) + (size_t)p.K * 12 +
                         (size_t)(p.hash_mask + 1) * 4;
+    // the limit is the kernel's, not the call's: one value, the largest, so that calls
+    // from several host threads cannot lower it under each other
+    constexpr size_t kMost = (CACHED ? (size_t)kDsMaxShare : 0) + (size_t)kDistillMaxTop * (12 + 2 * 4);
+    if (smem > kMost) return cudaErrorInvalidValue;
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
