@@ -515,6 +515,9 @@ int hqq_linear_adapters_backward(const void* dY, const void* X, int64_t M, const
  *    0, whatever its logits hold.
  *  - A logit of -inf has probability 0; a token whose logits are all -inf, or
  *    hold a NaN or +inf, gets NaN, and no other token does.
+ *  - The kernel's wait for a row is bounded (about a second); a token whose row has
+ *    not arrived by then gets a NaN lse and gradient (and loss, if it has an entry
+ *    with mass).
  *   logits     [in]  `dtype` [tokens, vocab], rows logits_stride elements apart
  *                    (>= vocab), aligned to its element.
  *   top_logits [in]  `top_dtype` [tokens, top_k], dense.

@@ -310,7 +310,13 @@ distill_kernel(const __grid_constant__ DistillParams p, int csize, int share_pac
     if constexpr (CACHED) {
         bool landed = false;
         for (int i = 0; i < kDsTries && !landed; ++i) landed = mbar_try(smem_u32(&bar), 0u);
-        if (!landed) mbar_wait(smem_u32(&bar), 0u, &abort_flag, nullptr, true);
+        if (!landed && !mbar_wait(smem_u32(&bar), 0u, &abort_flag, nullptr, true)) {
+            // the row did not arrive in time: no value of it is to be trusted, and NaN in
+            // one CTA's sum is NaN in every output of the token; the copy gets the same
+            // time once more before the CTA can end
+            s = __int_as_float(0x7fffffff);
+            mbar_wait(smem_u32(&bar), 0u, &abort_flag, nullptr, true);
+        }
     }
     if constexpr (CACHED) {
         // the packs at the row's ends, by the threads that own them in both passes
