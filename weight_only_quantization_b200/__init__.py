@@ -451,14 +451,29 @@ def _need(t, name, dev):
         raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
 
 
-def _run_on(dev, stream, fn, *args):
-    """fn(*args, stream) with CUDA device dev current, on the given stream of it (None:
-    its current one)."""
+def _on(stream, call, first, *args):
+    """call(first, *args) with ``stream`` as the current one.  The allocator hands out and
+    takes back memory in the order of one stream's work, so what the call allocates has
+    to be taken in that of its launches; results made there are, once freed, not handed
+    out before the work of that time on the stream that the caller is on has ended."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device.index != dev:
-        raise ValueError(f"stream must be on cuda:{dev}")
+    if first.get_device() != stream.device.index:
+        raise ValueError("stream must be on the tensors' device")
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return call(first, *args)
+    with torch.cuda.stream(stream):
+        out = call(first, *args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and not any(t is a for a in (first, *args)):
+            t.record_stream(current)
+    return out
+
+
+def _run_on(dev, fn, *args):
+    """fn(*args, stream) with CUDA device dev current, on its current stream."""
+    import torch
+    stream = torch.cuda.current_stream(dev)
     if torch.cuda.current_device() == dev:
         st = fn(*args, stream.cuda_stream)
     else:
@@ -479,6 +494,9 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
     token (0: the token is skipped).  ``grad`` is False, True, or the tensor to
     write the gradient to, which may be ``logits`` itself.  Returns
     (loss [tokens], lse [tokens], gradient or None)."""
+    if stream is not None:
+        return _on(stream, hqq_distill, logits, top_logits, top_index, temperature, teacher_lse,
+                   weight, grad, loss, lse)
     import torch
     if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA [tokens, vocab] tensor with adjacent columns")
@@ -516,7 +534,7 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
         grows = vocab if grad is None else grad.stride(0)
         if rows < vocab or grows < vocab:
             raise ValueError("rows of logits and grad must not overlap")
-    _run_on(dev, stream, _lib.hqq_distill, logits.data_ptr(), rows, dt, tokens, vocab,
+    _run_on(dev, _lib.hqq_distill, logits.data_ptr(), rows, dt, tokens, vocab,
             top_logits.data_ptr(), _dtype_code(top_logits.dtype, "top_logits"),
             top_index.data_ptr(), top_index.element_size(), top_logits.shape[1], temperature,
             _addr(teacher_lse), _addr(weight), loss.data_ptr(), lse.data_ptr(), _addr(grad), grows)
@@ -566,7 +584,7 @@ class Adapters:
 
 
 def _adapter_call(fn, lead, tail, x, q, adapters, index, zero_q, scale_q, M, backward, workspace,
-                  tensors, stream):
+                  tensors):
     """What both adapter calls check and marshal: fn(*lead, matrix, adapters, index, *tail,
     workspace, its bytes, stream)."""
     import torch
@@ -595,7 +613,7 @@ def _adapter_call(fn, lead, tail, x, q, adapters, index, zero_q, scale_q, M, bac
         workspace = x.new_empty(need, dtype=torch.uint8)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     byref = ctypes.byref
-    _run_on(dev, stream, fn, *lead, M, q.packed.data_ptr(), _addr(scale), _addr(zero),
+    _run_on(dev, fn, *lead, M, q.packed.data_ptr(), _addr(scale), _addr(zero),
             None if zero_q is None else byref(zero_q._c()),
             None if scale_q is None else byref(scale_q._c()), q.rows, q.cols, q.nbits, q.group,
             None if ca is None else byref(ca), _addr(index), *tail, _addr(workspace), nbytes)
@@ -608,6 +626,9 @@ def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, o
     int32 [M] tensor (negative or past the last: none), or None for adapter 0
     everywhere.  ``zero_q`` / ``scale_q`` replace q's zero / scale by their 8-bit
     form.  The workspace is allocated here unless given."""
+    if stream is not None:
+        return _on(stream, hqq_linear_adapters, X, q, adapters, index, out, status, workspace,
+                   zero_q, scale_q)
     import torch
     if X.dtype != torch.float16 or X.dim() != 2 or X.shape[1] != q.cols:
         raise ValueError("X must be a float16 [M, cols] tensor")
@@ -618,7 +639,7 @@ def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, o
         raise ValueError("out must be a float16 [M, rows] tensor")
     _adapter_call(_lib.hqq_linear_adapters, (X.data_ptr(),), (out.data_ptr(), _addr(status)), X, q,
                   adapters, index, zero_q, scale_q, M, 0, workspace,
-                  ((X, "X"), (out, "out"), (status, "status")), stream)
+                  ((X, "X"), (out, "out"), (status, "status")))
     return out
 
 
@@ -631,6 +652,9 @@ def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters |
     ``dY`` [M, rows] (see include/hqq.h): dX fp16 [M, cols], dA fp32 [count, rank,
     cols], dB fp32 [count, rows, rank].  Without adapters (X may then be None),
     or for what need_dX / need_factors leaves out, None is returned in its place."""
+    if stream is not None:
+        return _on(stream, hqq_linear_adapters_backward, dY, X, q, adapters, index, need_dX,
+                   need_factors, dX, dA, dB, status, workspace, zero_q, scale_q)
     import torch
     if dY.dtype != torch.float16 or dY.dim() != 2 or dY.shape[1] != q.rows:
         raise ValueError("dY must be a float16 [M, rows] tensor")
@@ -664,6 +688,5 @@ def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters |
     _adapter_call(_lib.hqq_linear_adapters_backward, (dY.data_ptr(), _addr(X)),
                   (_addr(dX), _addr(dA), _addr(dB), _addr(status)), dY, q, adapters, index, zero_q,
                   scale_q, M, 1, workspace,
-                  ((dY, "dY"), (X, "X"), (dX, "dX"), (dA, "dA"), (dB, "dB"), (status, "status")),
-                  stream)
+                  ((dY, "dY"), (X, "X"), (dX, "dX"), (dA, "dA"), (dB, "dB"), (status, "status")))
     return dX, dA, dB
