@@ -56,7 +56,7 @@ def env(monkeypatch):
 
     class Lib:
         def __getattr__(self, name):
-            if name.endswith("_bytes"):
+            if name.endswith(("_bytes", "_groups")):
                 return getattr(real, name)
             return lambda *args: calls.append(args) or 0
     real = hqq._lib
@@ -99,6 +99,63 @@ def test_adapter_calls(env):
 def test_distill(env):
     z, top, at = tensor(4, 100), tensor(4, 5), tensor(4, 5, dtype=torch.int64)
     check(env, env.hqq.hqq_distill(z, top, at, grad=True, stream=env.side))
+
+
+# (results stay with the caller; what torch.empty makes is seen when it is held)
+CALLS = {
+    "quantize": lambda h, s: h.hqq_quantize(tensor(64, 128), stream=s),
+    "quantize_ex": lambda h, s: h.hqq_quantize_ex(tensor(64, 128), stream=s),
+    "quantize_half": lambda h, s: h.hqq_quantize_ex(tensor(64, 128), stream=s, precision="fp16"),
+    "dequantize": lambda h, s: h.hqq_dequantize(matrix(h), stream=s),
+    "meta_quantize": lambda h, s: h.hqq_meta_quantize(tensor(128), 16, stream=s),
+    "meta_batch": lambda h, s: h.hqq_meta_quantize_batch([(tensor(128), 0), (tensor(64), 16)],
+                                                         stream=s),
+    "meta_dequantize": lambda h, s: h.hqq_meta_dequantize(meta(), stream=s),
+    "dequantize_meta": lambda h, s: h.hqq_dequantize_meta(
+        tensor(64 * 64, dtype=torch.uint8), meta(), 64, 128, 4, 64, scale=tensor(64, 2), stream=s),
+    "linear": lambda h, s: h.hqq_linear(tensor(3, 128), matrix(h), stream=s),
+    "linear_meta": lambda h, s: h.hqq_linear_meta(
+        tensor(3, 128), tensor(64 * 64, dtype=torch.uint8), meta(), 64, 128, 4, 64,
+        scale=tensor(64, 2), stream=s),
+    "lowrank": lambda h, s: h.hqq_lowrank(tensor(64, 128), matrix(h), 8,
+                                          tensor(128, 16, dtype=torch.float32), stream=s),
+}
+
+
+def flat(result):
+    if isinstance(result, torch.Tensor):
+        yield result
+    elif result is not None and not isinstance(result, (int, float)):
+        for r in result if isinstance(result, (tuple, list)) else vars(result).values():
+            yield from flat(r)
+
+
+def meta():
+    import weight_only_quantization_b200 as hqq
+    return hqq.Meta8(tensor(128, dtype=torch.uint8), tensor(1), tensor(1), 0)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_earlier_calls(env, name, monkeypatch):
+    """The library is called with the side stream current, all that the call made was
+    made then, and its results are held for the main stream."""
+    made = {}
+
+    def empty(*args, device=None, **kwargs):
+        t = real(*args, **kwargs).as_subclass(OnDevice)
+        made[t.data_ptr()] = (OnDevice.current, t)
+        return t
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", empty)
+    result = CALLS[name](env.hqq, env.side)
+    results = list(flat(result))
+    assert made and results and len(env.calls) == 1
+    mine = {t.data_ptr() for t in results}
+    for at, (s, _) in made.items():
+        assert s is env.side
+        assert OnDevice.held.get(at, []) == ([env.main] if at in mine else [])
+    assert mine <= set(made) and OnDevice.current is env.main
+    assert len(made) == len(mine) + (name == "lowrank")          # its workspace
 
 
 def test_the_current_stream_given_is_no_other_stream(env):

@@ -124,11 +124,9 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream():
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _check(st: int):
@@ -150,6 +148,37 @@ class QuantizedMatrix:
     iters: "torch.Tensor | None" = None
     err: "torch.Tensor | None" = None
     half: "torch.Tensor | None" = None      # uint8: group solved in half precision
+
+
+def _tensors(result):
+    """The tensors of what a call returns."""
+    if isinstance(result, (tuple, list)):
+        for r in result:
+            yield from _tensors(r)
+    elif isinstance(result, (QuantizedMatrix, Meta8)):
+        yield from _tensors(list(vars(result).values()))
+    elif hasattr(result, "record_stream"):
+        yield result
+
+
+def _on(stream, on, call, *args):
+    """call(*args) with ``stream`` as the current one (``on``: a tensor of the call).  The
+    allocator hands out and takes back memory in the order of one stream's work, so what
+    the call allocates has to be taken in that of its launches; results made there are,
+    once freed, not handed out before the work of that time on the stream that the caller
+    is on has ended."""
+    import torch
+    if on.get_device() != stream.device.index:
+        raise ValueError("stream must be on the tensors' device")
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return call(*args)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in _tensors(out):
+        if not any(t is a for a in args):
+            t.record_stream(current)
+    return out
 
 
 def _outputs(W, nbits, group, packed, scale, zero):
@@ -184,6 +213,9 @@ def hqq_quantize(W, nbits: int = 4, group: int = 64, p: float = DEFAULT_P,
                  stream=None, precision: str = "fp32") -> QuantizedMatrix:
     """Quantize a contiguous fp16 CUDA matrix [rows, cols] (see include/hqq.h);
     ``precision="fp16"`` runs the half-precision solver (hqq_quantize_half)."""
+    if stream is not None:
+        return _on(stream, W, hqq_quantize, W, nbits, group, p, beta, kappa, iters, packed, scale,
+                   zero, None, precision)
     import torch
     if W.dtype != torch.float16 or W.dim() != 2:
         raise ValueError("W must be a 2-D float16 tensor")
@@ -195,10 +227,10 @@ def hqq_quantize(W, nbits: int = 4, group: int = 64, p: float = DEFAULT_P,
     if half:
         _check(_lib.hqq_quantize_half(_ptr(W), rows, cols, nbits, group, p, beta, kappa, iters,
                                       _ptr(packed), _ptr(scale), _ptr(zero), None, None, None,
-                                      None, _stream(stream)))
+                                      None, _stream()))
     else:
         _check(_lib.hqq_quantize(_ptr(W), rows, cols, nbits, group, p, beta, kappa, iters,
-                                 _ptr(packed), _ptr(scale), _ptr(zero), _stream(stream)))
+                                 _ptr(packed), _ptr(scale), _ptr(zero), _stream()))
     return QuantizedMatrix(packed, scale, zero, rows, cols, nbits, group)
 
 
@@ -210,6 +242,9 @@ def hqq_quantize_ex(W, nbits: int = 4, group: int = 64, p: float = DEFAULT_P,
     """hqq_quantize plus the fp32 zero, the solver's l_p error and the
     accepted-iteration count of every group (and, with ``precision="fp16"``,
     which groups were solved in half precision)."""
+    if stream is not None:
+        return _on(stream, W, hqq_quantize_ex, W, nbits, group, p, beta, kappa, iters, packed,
+                   scale, zero, zero_f32, iters_out, err_out, None, precision, half_out)
     import torch
     if W.dtype != torch.float16 or W.dim() != 2:
         raise ValueError("W must be a 2-D float16 tensor")
@@ -233,25 +268,27 @@ def hqq_quantize_ex(W, nbits: int = 4, group: int = 64, p: float = DEFAULT_P,
         _check(_lib.hqq_quantize_half(_ptr(W), rows, cols, nbits, group, p, beta, kappa, iters,
                                       _ptr(packed), _ptr(scale), _ptr(zero), _ptr(zero_f32),
                                       _ptr(err_out), _ptr(iters_out), _ptr(half_out),
-                                      _stream(stream)))
+                                      _stream()))
     else:
         half_out = None
         _check(_lib.hqq_quantize_ex(_ptr(W), rows, cols, nbits, group, p, beta, kappa, iters,
                                     _ptr(packed), _ptr(scale), _ptr(zero), _ptr(zero_f32),
-                                    _ptr(err_out), _ptr(iters_out), _stream(stream)))
+                                    _ptr(err_out), _ptr(iters_out), _stream()))
     return QuantizedMatrix(packed, scale, zero, rows, cols, nbits, group, zero_f32, iters_out,
                            err_out, half_out)
 
 
 def hqq_dequantize(q: QuantizedMatrix, out=None, stream=None):
     """fp16 [rows, cols] = (code - zero) * scale  (see include/hqq.h)."""
+    if stream is not None:
+        return _on(stream, q.packed, hqq_dequantize, q, out)
     import torch
     for t, n in ((q.packed, "packed"), (q.scale, "scale"), (q.zero, "zero"), (out, "out")):
         _check_tensor(t, n)
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=torch.float16, device=q.packed.device)
     _check(_lib.hqq_dequantize(_ptr(q.packed), _ptr(q.scale), _ptr(q.zero), q.rows, q.cols,
-                               q.nbits, q.group, _ptr(out), _stream(stream)))
+                               q.nbits, q.group, _ptr(out), _stream()))
     return out
 
 
@@ -279,6 +316,8 @@ def hqq_meta_quantize(x, mgroup: int = 0, codes=None, scale=None, zero=None,
                       stream=None) -> Meta8:
     """8-bit min-max round-to-nearest of an fp16 meta tensor (flat order;
     ``mgroup`` consecutive values per group, 0 = one group); see include/hqq.h."""
+    if stream is not None:
+        return _on(stream, x, hqq_meta_quantize, x, mgroup, codes, scale, zero)
     import torch
     if x.dtype != torch.float16:
         raise ValueError("x must be float16")
@@ -294,7 +333,7 @@ def hqq_meta_quantize(x, mgroup: int = 0, codes=None, scale=None, zero=None,
     for t, nm in ((codes, "codes"), (scale, "scale"), (zero, "zero")):
         _check_tensor(t, nm)
     _check(_lib.hqq_meta_quantize(_ptr(x), n, mgroup, _ptr(codes), _ptr(scale), _ptr(zero),
-                                  _stream(stream)))
+                                  _stream()))
     return Meta8(codes, scale, zero, mgroup)
 
 
@@ -302,6 +341,8 @@ def hqq_meta_quantize_batch(tensors, stream=None, outputs=None) -> list:
     """hqq_meta_quantize of many fp16 meta tensors in shared launches.
     ``tensors`` is a list of (x, mgroup); ``outputs`` optionally a list of
     Meta8 to write into (same order).  Returns the list of Meta8."""
+    if stream is not None and tensors:
+        return _on(stream, tensors[0][0], hqq_meta_quantize_batch, tensors, None, outputs)
     import torch
     out = []
     jobs = (_CMetaJob * max(len(tensors), 1))()
@@ -322,12 +363,14 @@ def hqq_meta_quantize_batch(tensors, stream=None, outputs=None) -> list:
         jobs[i] = _CMetaJob(x.data_ptr(), n, mgroup, m.codes.data_ptr(), m.scale.data_ptr(),
                             m.zero.data_ptr())
         out.append(m)
-    _check(_lib.hqq_meta_quantize_batch(jobs, len(tensors), _stream(stream)))
+    _check(_lib.hqq_meta_quantize_batch(jobs, len(tensors), _stream()))
     return out
 
 
 def hqq_meta_dequantize(m: Meta8, out=None, stream=None):
     """fp16 [n] = (code - zero) * scale per value of an 8-bit meta tensor."""
+    if stream is not None:
+        return _on(stream, m.codes, hqq_meta_dequantize, m, out)
     import torch
     for t, nm in ((m.codes, "codes"), (m.scale, "scale"), (m.zero, "zero"), (out, "out")):
         _check_tensor(t, nm)
@@ -335,7 +378,7 @@ def hqq_meta_dequantize(m: Meta8, out=None, stream=None):
     if out is None:
         out = torch.empty(n, dtype=torch.float16, device=m.codes.device)
     _check(_lib.hqq_meta_dequantize(_ptr(m.codes), _ptr(m.scale), _ptr(m.zero), n, m.group,
-                                    _ptr(out), _stream(stream)))
+                                    _ptr(out), _stream()))
     return out
 
 
@@ -343,6 +386,9 @@ def hqq_dequantize_meta(packed, zero_q: Meta8, rows: int, cols: int, nbits: int,
                         scale=None, scale_q: Meta8 | None = None, out=None, stream=None):
     """Dequantize a matrix whose zero points (and optionally scales) are kept in
     8-bit form, in one pass (see include/hqq.h)."""
+    if stream is not None:
+        return _on(stream, packed, hqq_dequantize_meta, packed, zero_q, rows, cols, nbits, group,
+                   scale, scale_q, out)
     import torch
     for t, nm in ((packed, "packed"), (scale, "scale"), (out, "out")):
         _check_tensor(t, nm)
@@ -352,7 +398,7 @@ def hqq_dequantize_meta(packed, zero_q: Meta8, rows: int, cols: int, nbits: int,
     sc = scale_q._c() if scale_q is not None else None
     _check(_lib.hqq_dequantize_meta(_ptr(packed), ctypes.byref(zc), _ptr(scale),
                                     ctypes.byref(sc) if sc is not None else None,
-                                    rows, cols, nbits, group, _ptr(out), _stream(stream)))
+                                    rows, cols, nbits, group, _ptr(out), _stream()))
     return out
 
 
@@ -362,6 +408,8 @@ def hqq_linear(X, q: QuantizedMatrix, out=None, status=None, stream=None):
     include/hqq.h).  ``status`` is an optional int32 CUDA tensor of one element
     (cleared by the caller) that the kernel sets to 1 if an internal wait ran
     out."""
+    if stream is not None:
+        return _on(stream, X, hqq_linear, X, q, out, status)
     import torch
     if X.dtype != torch.float16 or X.dim() != 2 or X.shape[1] != q.cols:
         raise ValueError("X must be a float16 [M, cols] tensor")
@@ -372,7 +420,7 @@ def hqq_linear(X, q: QuantizedMatrix, out=None, status=None, stream=None):
         out = torch.empty((X.shape[0], q.rows), dtype=torch.float16, device=X.device)
     _check(_lib.hqq_linear(_ptr(X), X.shape[0], _ptr(q.packed), _ptr(q.scale), _ptr(q.zero),
                            q.rows, q.cols, q.nbits, q.group, _ptr(out), _ptr(status),
-                           _stream(stream)))
+                           _stream()))
     return out
 
 
@@ -381,6 +429,9 @@ def hqq_linear_meta(X, packed, zero_q: Meta8, rows: int, cols: int, nbits: int, 
                     stream=None):
     """hqq_linear for a matrix whose zero points (and optionally scales) are
     kept in 8-bit form; they are restored inside the kernel (see include/hqq.h)."""
+    if stream is not None:
+        return _on(stream, X, hqq_linear_meta, X, packed, zero_q, rows, cols, nbits, group, scale,
+                   scale_q, out, status)
     import torch
     if X.dtype != torch.float16 or X.dim() != 2 or X.shape[1] != cols:
         raise ValueError("X must be a float16 [M, cols] tensor")
@@ -394,7 +445,7 @@ def hqq_linear_meta(X, packed, zero_q: Meta8, rows: int, cols: int, nbits: int, 
     _check(_lib.hqq_linear_meta(_ptr(X), X.shape[0], _ptr(packed), ctypes.byref(zc),
                                 _ptr(scale), ctypes.byref(sc) if sc is not None else None,
                                 rows, cols, nbits, group, _ptr(out), _ptr(status),
-                                _stream(stream)))
+                                _stream()))
     return out
 
 
@@ -404,6 +455,8 @@ def hqq_lowrank(W, q: QuantizedMatrix, rank: int, omega, power_iters: int = 2, w
     error W - W_hat, with the r leading singular values (see include/hqq.h).
     ``omega`` is the fp32 [cols, sketch] Gaussian test matrix (sketch 16, 32 or
     64), drawn by the caller; the workspace is allocated here unless given."""
+    if stream is not None:
+        return _on(stream, W, hqq_lowrank, W, q, rank, omega, power_iters, workspace)
     import torch
     if W.dtype != torch.float16 or tuple(W.shape) != (q.rows, q.cols):
         raise ValueError("W must be the float16 [rows, cols] matrix that q quantizes")
@@ -423,7 +476,7 @@ def hqq_lowrank(W, q: QuantizedMatrix, rank: int, omega, power_iters: int = 2, w
     _check(_lib.hqq_lowrank(_ptr(W), _ptr(q.packed), _ptr(q.scale), _ptr(q.zero), q.rows, q.cols,
                             q.nbits, q.group, rank, sketch, power_iters, _ptr(omega), _ptr(B),
                             _ptr(A), _ptr(sigma), _ptr(workspace), workspace.numel(),
-                            _stream(stream)))
+                            _stream()))
     return B, A, sigma
 
 
@@ -451,25 +504,6 @@ def _need(t, name, dev):
         raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
 
 
-def _on(stream, call, first, *args):
-    """call(first, *args) with ``stream`` as the current one.  The allocator hands out and
-    takes back memory in the order of one stream's work, so what the call allocates has
-    to be taken in that of its launches; results made there are, once freed, not handed
-    out before the work of that time on the stream that the caller is on has ended."""
-    import torch
-    if first.get_device() != stream.device.index:
-        raise ValueError("stream must be on the tensors' device")
-    current = torch.cuda.current_stream(stream.device)
-    if stream == current:
-        return call(first, *args)
-    with torch.cuda.stream(stream):
-        out = call(first, *args)
-    for t in out if isinstance(out, tuple) else (out,):
-        if t is not None and not any(t is a for a in (first, *args)):
-            t.record_stream(current)
-    return out
-
-
 def _run_on(dev, fn, *args):
     """fn(*args, stream) with CUDA device dev current, on its current stream."""
     import torch
@@ -495,8 +529,8 @@ def hqq_distill(logits, top_logits, top_index, temperature: float = 1.0, teacher
     write the gradient to, which may be ``logits`` itself.  Returns
     (loss [tokens], lse [tokens], gradient or None)."""
     if stream is not None:
-        return _on(stream, hqq_distill, logits, top_logits, top_index, temperature, teacher_lse,
-                   weight, grad, loss, lse)
+        return _on(stream, logits, hqq_distill, logits, top_logits, top_index, temperature,
+                   teacher_lse, weight, grad, loss, lse)
     import torch
     if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA [tokens, vocab] tensor with adjacent columns")
@@ -627,7 +661,7 @@ def hqq_linear_adapters(X, q: QuantizedMatrix, adapters: Adapters, index=None, o
     everywhere.  ``zero_q`` / ``scale_q`` replace q's zero / scale by their 8-bit
     form.  The workspace is allocated here unless given."""
     if stream is not None:
-        return _on(stream, hqq_linear_adapters, X, q, adapters, index, out, status, workspace,
+        return _on(stream, X, hqq_linear_adapters, X, q, adapters, index, out, status, workspace,
                    zero_q, scale_q)
     import torch
     if X.dtype != torch.float16 or X.dim() != 2 or X.shape[1] != q.cols:
@@ -653,7 +687,7 @@ def hqq_linear_adapters_backward(dY, X, q: QuantizedMatrix, adapters: Adapters |
     cols], dB fp32 [count, rows, rank].  Without adapters (X may then be None),
     or for what need_dX / need_factors leaves out, None is returned in its place."""
     if stream is not None:
-        return _on(stream, hqq_linear_adapters_backward, dY, X, q, adapters, index, need_dX,
+        return _on(stream, dY, hqq_linear_adapters_backward, dY, X, q, adapters, index, need_dX,
                    need_factors, dX, dA, dB, status, workspace, zero_q, scale_q)
     import torch
     if dY.dtype != torch.float16 or dY.dim() != 2 or dY.shape[1] != q.rows:
