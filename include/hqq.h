@@ -533,8 +533,8 @@ int hqq_linear_adapters_backward(const void* dY, const void* X, int64_t M, const
  * below 2^27.  The kernel is fastest where logits, grad and their rows are
  * 16-byte aligned.
  * Errors: HQQ_ERR_SHAPE, HQQ_ERR_UNSUPPORTED (dtype, index_bytes),
- * HQQ_ERR_PARAM (temperature not > 0 and finite), HQQ_ERR_NULL, HQQ_ERR_ALIGN,
- * HQQ_ERR_CUDA.
+ * HQQ_ERR_PARAM (temperature not > 0 and finite, or log2(e) / temperature beyond
+ * fp32), HQQ_ERR_NULL, HQQ_ERR_ALIGN, HQQ_ERR_CUDA.
  */
 int hqq_distill(const void* logits, int64_t logits_stride, int dtype, int64_t tokens,
                 int64_t vocab, const void* top_logits, int top_dtype, const void* top_index,

@@ -535,7 +535,11 @@ extern "C" int hqq_distill(const void* logits, int64_t logits_stride, int dtype,
         return HQQ_ERR_SHAPE;
     if (!dtype_ok(dtype) || !dtype_ok(top_dtype) || (index_bytes != 4 && index_bytes != 8))
         return HQQ_ERR_UNSUPPORTED;
-    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+    // (1 / t and log2(e) / t as the kernel takes them; infinite, they would make NaN of 0)
+    const float inv_t = 1.0f / temperature;
+    const float log2e_t = (float)(1.4426950408889634 / (double)temperature);
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(inv_t) ||
+        !std::isfinite(log2e_t))
         return HQQ_ERR_PARAM;
     if (logits_stride < vocab || logits_stride > ((int64_t)1 << 40) ||
         (grad && (grad_stride < vocab || grad_stride > ((int64_t)1 << 40))))
@@ -568,8 +572,8 @@ extern "C" int hqq_distill(const void* logits, int64_t logits_stride, int dtype,
     p.at64 = index_bytes == 8;
     p.hash_mask = 63;
     while (p.hash_mask < 2 * (int)top_k - 1) p.hash_mask = 2 * p.hash_mask + 1;
-    p.inv_t = 1.0f / temperature;
-    p.log2e_t = (float)(1.4426950408889634 / (double)temperature);
+    p.inv_t = inv_t;
+    p.log2e_t = log2e_t;
     const cudaError_t err = launch_distill(p, dtype, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
 }
