@@ -551,7 +551,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Li
     const bool epi = warp >= 2;
     const int grp = (warp - 2) >> 2;
     const int f = 32 * (warp & 3) + lane;                // feature within the tile
-    const int64_t nf = n0 + f, nfc = nf < features ? nf : features - 1;
+    const int64_t nf = n0 + f;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float* xbuf = reinterpret_cast<float*>(smem);        // the other parts' sums
     const int win = ks > 1 && bn > kGmWindow ? kGmWindow : bn;
