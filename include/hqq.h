@@ -510,11 +510,13 @@ int hqq_linear_adapters_backward(const void* dY, const void* X, int64_t M, const
  * logits' type.  Results do not depend on execution order.
  *  - An index may occur several times: its p_k add up in the gradient, and the
  *    loss takes each entry as given.  An entry whose value is -inf has p_k = 0.
- *  - A token without a valid entry has loss 0 and gradient 0.
+ *  - A token without a valid entry has loss 0 and (its logits finite or -inf, not all
+ *    -inf) gradient 0.
  *  - A token of weight 0 (padding, prompt) is not read: loss 0, lse 0, gradient
  *    0, whatever its logits hold.
  *  - A logit of -inf has probability 0; a token whose logits are all -inf, or
- *    hold a NaN or +inf, gets NaN, and no other token does.
+ *    hold a NaN or +inf, gets NaN in its gradient and, if it has an entry with mass,
+ *    its loss, and no other token does.
  *  - The kernel's wait for a row is bounded (about a second); a token whose row has
  *    not arrived by then gets a NaN lse and gradient (and loss, if it has an entry
  *    with mass).
