@@ -82,3 +82,25 @@ def test_memory_that_the_current_stream_still_reads(calls, name):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(copies, want))
         del junk
+
+
+def test_a_stream_as_a_bare_handle(calls):
+    """Any object that has a stream's handle is taken as that stream."""
+    import types
+
+    import weight_only_quantization_b200 as hqq
+    side = torch.cuda.Stream()
+    bare = types.SimpleNamespace(cuda_stream=side.cuda_stream)
+    for call in calls.values():
+        want = call()
+        torch.cuda.synchronize()
+        got = call(bare)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    q, _ = matrix(hqq, 264, 512, 3, 64, seed=7)
+    X = tokens(4, 512, 6).cuda()
+    want = hqq.hqq_linear(X, q)
+    torch.cuda.synchronize()
+    got = hqq.hqq_linear(X, q, stream=bare)
+    side.synchronize()
+    assert torch.equal(got, want)

@@ -168,7 +168,9 @@ def _on(stream, on, call, *args):
     once freed, not handed out before the work of that time on the stream that the caller
     is on has ended."""
     import torch
-    if on.get_device() != stream.device.index:
+    if on.is_cuda and not hasattr(stream, "device"):     # (any object that has a handle)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=on.device)
+    if not on.is_cuda or on.get_device() != stream.device.index:
         raise ValueError("stream must be on the tensors' device")
     current = torch.cuda.current_stream(stream.device)
     if stream == current:
